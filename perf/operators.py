@@ -147,6 +147,16 @@ def work(case):
 
 
 # ---------------------------------------------------------------- state
+class _Handle:
+    """A pool of the library, destroyed with the last tensor that looks into it."""
+
+    def __init__(self, pk, *args):
+        self.destroy, self.value = pk.pool_destroy, pk.pool_create(*args)
+
+    def __del__(self):
+        self.destroy(self.value)
+
+
 class _Pool:
     """The paged buffers: the library's pool, or torch tensors of the same layout."""
 
@@ -155,18 +165,17 @@ class _Pool:
         self.handle = None
         if own:
             import paged_kv_chunk_query_b200 as pk
-            self.destroy = pk.pool_destroy
-            self.handle = pk.pool_create(pages, case["page"], case["hkv"], case["d"],
-                                         pk.LOC_DEVICE, grad, 0, torch.cuda.current_device())
+            owner = _Handle(pk, pages, case["page"], case["hkv"], case["d"], pk.LOC_DEVICE, grad,
+                            0, torch.cuda.current_device())
+            self.handle = owner.value
             self.kv, self.grad, self.mean = pk.pool_views(self.handle)
+            for view in (self, self.kv, self.grad, self.mean):  # views borrow the pool's memory
+                if view is not None:
+                    view.owner = owner
         else:
             self.kv = torch.zeros(shape, dtype=torch.bfloat16, device=DEVICE)
             self.grad = torch.zeros(shape, dtype=torch.float32, device=DEVICE) if grad else None
             self.mean = torch.zeros((pages, case["hkv"], case["d"]), device=DEVICE)
-
-    def __del__(self):
-        if self.handle:
-            self.destroy(self.handle)
 
 
 def _i32(x):
