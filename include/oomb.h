@@ -212,6 +212,123 @@ typedef enum oomb_bwd_step {
 oomb_status oomb_chunk_attn_bwd_step(oomb_pool* pool, const oomb_attn_args* args, int32_t step,
                                      void* stream);
 
+/* ---------------------------------------------------------------- ragged append
+ * oomb_kv_append_rope: keys and values of a ragged batch of new tokens into
+ * their sequences' pages, with the position rotation (RoPE) applied to keys
+ * and queries on the way.  It serves single tokens (one per sequence, while
+ * decoding), prompts of any length and whole training chunks; oomb_kv_append
+ * above takes page-aligned chunks of keys that are rotated already.
+ *   Sequence b owns tokens [seq_start[b], seq_start[b+1]) of the batch and the
+ *   pages page_tables[b]; it holds cached_lens[b] tokens before the call.  Its
+ *   j-th new token goes to cache position c = cached_lens[b] + j, row c %
+ *   page_size of page page_tables[b][c / page_size].  A token at position p
+ *   (positions[t], any int32; it need not be its cache position) is rotated in
+ *   each of rotary_dim / 2 pairs (x_a, x_b) of a head by the angle p f_i, f_i =
+ *   inv_freq[i]:   x_a cos - x_b sin,  x_b cos + x_a sin,
+ *   with pair i = (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved;
+ *   values from rotary_dim on are left as they are.  The angle is reduced in 64
+ *   bits, so a position of 2^20 or 2^30 loses nothing; cos and sin are rounded
+ *   to fp32, the products and the sum are fp32, the result is rounded to bf16.
+ *   Writes the rotated keys and the values into the pages, the rotated queries
+ *   to q_out, zeroes the gradient rows of the new tokens (if the pool has
+ *   gradients), and sets the representative of every page that received a
+ *   token to the fp32 mean of the keys in rows [0, r], r the last row written:
+ *   the page means that oomb_page_topk scores, also for a page not yet full.
+ *   Tokens outside every sequence (before seq_start[0], from seq_start[n_seqs]
+ *   on: the padding of a fixed-size batch) are skipped and their rows of q_out
+ *   stay as they were.  A token whose page id is outside the pool sets bit 0 of
+ *   the device status word; one whose page index is outside [0, max_pages), a
+ *   negative cached_lens and a seq_start that decreases or leaves [0, n_tokens]
+ *   set bit 2.  Such tokens' keys and values are skipped.
+ * Two tokens of one call must not share a cache position, and pages that one
+ * call writes must belong to one sequence each.  Two launches.
+ *
+ * oomb_kv_append_rope_bwd: its backward, the step between attention's
+ * gradients and the projection's: for the same tokens,
+ *   dq_out = R(-p) dq,  dk = R(-p) (the page's dK row),  dv = the page's dV row,
+ * read from the pool's fp32 gradient blocks, in fp32 and rounded to bf16 once.
+ * The same fields of the arguments: k and v are the outputs dk and dv, q is
+ * the input dq (as oomb_chunk_attn_bwd writes it) and q_out the output.  The
+ * gradient blocks stay as they are.  A token skipped by the rules above leaves
+ * its rows of dk and dv as they were.  One launch; needs a pool with gradients.
+ *
+ * Rows of k, v, q and q_out are [heads][head_dim], dense, and start
+ * *_stride elements apart (a multiple of 8, at least heads * head_dim; the
+ * parts of a fused projection's output can be passed in place).  16-byte
+ * aligned.  q_out may be q itself with the same stride; otherwise buffers must
+ * not overlap.  q and q_out may both be NULL (num_q_heads is then ignored).
+ * Requires a device pool; rotary_dim a multiple of 16 in [0, head_dim]
+ * (OOMB_ERR_UNSUPPORTED otherwise; inv_freq may be NULL when it is 0).
+ * n_tokens == 0 or n_seqs == 0 is a no-op. */
+typedef struct oomb_rope_args {
+  const int32_t* seq_start;   /* device int32 [n_seqs + 1], ascending              */
+  const int32_t* cached_lens; /* device int32 [n_seqs]                             */
+  const int32_t* page_tables; /* device int32 [n_seqs][max_pages] physical ids     */
+  const int32_t* positions;   /* device int32 [n_tokens]                           */
+  const float* inv_freq;      /* device fp32 [rotary_dim / 2]                      */
+  void* k;                    /* device bf16 [n_tokens] rows of num_kv_heads heads */
+  void* v;                    /* the same                                          */
+  const void* q;              /* device bf16 [n_tokens] rows of num_q_heads heads  */
+  void* q_out;                /* the same                                          */
+  int64_t k_stride, v_stride, q_stride, q_out_stride; /* elements from row to row  */
+  int32_t n_tokens, n_seqs, max_pages;
+  int32_t num_q_heads;
+  int32_t rotary_dim;
+  int32_t interleaved;        /* 0: pairs (i, i + rotary_dim / 2); 1: (2i, 2i + 1) */
+} oomb_rope_args;
+oomb_status oomb_kv_append_rope(oomb_pool* pool, const oomb_rope_args* args, void* stream);
+oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args, void* stream);
+
+/* ---------------------------------------------------------------- single-token attention
+ * oomb_decode_attn: one query token per sequence attends to the tokens of the
+ * sequence's own pages and, if it is in a prefix group, to the group's prefix,
+ * whose pages are stored once and read once for all sequences of the group:
+ *   S_j = scale q.k_j over both,  LSE = ln sum_j exp(S_j),  O = sum_j exp(S_j - LSE) v_j.
+ * Sequence b has seq_lens[b] own tokens (0 allowed) in the pages page_tables[b]
+ * in order; the last page may be partly filled, what its other rows hold
+ * (infinities and NaN included) has no influence.  The token's own key and
+ * value are among them once oomb_kv_append_rope has put them there.  Prefix
+ * group j covers sequences [group_start[j], group_start[j+1]) and has
+ * prefix_lens[j] tokens (0 allowed, any length: own tokens start on a page of
+ * their own) in the pages prefix_pages[j]; sequences before group_start[0] and
+ * from group_start[n_groups] on have no prefix.  The prefix and a sequence's
+ * own pages may share pages.  A sequence without any token gets O = 0 and
+ * LSE = -inf.
+ * P is rounded to bf16 for the product with V; S, the running maximum and sum,
+ * O and the merge of the parts are fp32.  Results do not depend on what else
+ * runs and are the same bits in every call on the same inputs.
+ * Lengths and group starts are read on the device, so a captured graph replays
+ * with new ones.  A length outside [0, max_pages * page_size] is clamped, a
+ * group_start that decreases or leaves [0, n_seqs] is clamped to the previous
+ * group's end or to n_seqs, both setting bit 2 of the device status word; a
+ * page id outside the pool sets bit 0 and its tokens are skipped.
+ * Requires a device pool, num_q_heads a multiple of num_kv_heads, softmax_scale
+ * > 0, n_seqs <= 65535, n_groups <= n_seqs, rows of q and o dense [heads][head_dim],
+ * 16-byte aligned, *_stride elements apart (a multiple of 8).  o may be q.
+ * The workspace (oomb_decode_attn_workspace_size() bytes, 16-byte aligned) needs
+ * no initialisation; calls sharing one must be ordered (one stream).  n_seqs ==
+ * 0 is a no-op. */
+typedef struct oomb_decode_args {
+  const void* q;               /* device bf16 [n_seqs] rows of num_q_heads heads    */
+  void* o;                     /* the same: output                                  */
+  float* lse;                  /* device fp32 [n_seqs][num_q_heads]; may be NULL    */
+  int64_t q_stride, o_stride;  /* elements from row to row                          */
+  const int32_t* page_tables;  /* device int32 [n_seqs][max_pages] physical ids     */
+  const int32_t* seq_lens;     /* device int32 [n_seqs], own tokens                 */
+  const int32_t* prefix_pages; /* device int32 [n_groups][max_prefix_pages]         */
+  const int32_t* prefix_lens;  /* device int32 [n_groups]                           */
+  const int32_t* group_start;  /* device int32 [n_groups + 1], ascending            */
+  int32_t n_seqs, num_q_heads, max_pages;
+  int32_t n_groups, max_prefix_pages; /* n_groups 0: no prefixes                    */
+  float softmax_scale;
+  void* workspace;
+  size_t workspace_bytes;
+} oomb_decode_args;
+oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args* args, void* stream);
+/* Bytes of its workspace on the current device; 0 for arguments that it refuses. */
+size_t oomb_decode_attn_workspace_size(int32_t n_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t n_groups);
+
 /* ---------------------------------------------------------------- projection
  * Q/K/V projection of one chunk with a paged epilogue ([pt] §2D: the pages a
  * sparse chunk needs are known once its queries exist, so their transfer can

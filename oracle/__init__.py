@@ -25,6 +25,8 @@ Modules
   sparse     page representatives, group query means, Top-K page choice
   recurrent  the chunk-by-chunk loop over a whole sequence
   pool       the page allocator's free-list policy (SplitMix64 + Fisher-Yates)
+  rope       the position rotation of heads and its inverse
+  decode     attention of one query token per sequence over explicit keys
 
 Every function here is pinned by tests under ``tests/test_oracle_*.py`` to
 facts other than itself (closed forms, finite differences, invariants, brute

@@ -41,7 +41,8 @@ EXPORTS = (
     "oomb_block_copy", "oomb_grad_block_add", "oomb_prefetch_lists", "oomb_local_pages",
     "oomb_qkv_project", "oomb_selftest_writeback_copy", "oomb_qpage_lists",
     "oomb_page_topk_qsum_workspace_size", "oomb_page_topk_qsum",
-    "oomb_chunk_attn_fwd_workspace_size",
+    "oomb_chunk_attn_fwd_workspace_size", "oomb_kv_append_rope", "oomb_kv_append_rope_bwd",
+    "oomb_decode_attn", "oomb_decode_attn_workspace_size",
 )
 
 
@@ -68,6 +69,30 @@ class AttnArgs(ctypes.Structure):
                 ("lists_per_qtile", ctypes.c_int32), ("segment", ctypes.c_int32),
                 ("o_acc", ctypes.c_void_p), ("dq_acc", ctypes.c_void_p),
                 ("past_masks", ctypes.c_void_p), ("fwd_ws", ctypes.c_void_p)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("seq_start", ctypes.c_void_p), ("cached_lens", ctypes.c_void_p),
+                ("page_tables", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class DecodeArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+                ("page_tables", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("prefix_pages", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("group_start", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("max_prefix_pages", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 _lib = None
@@ -114,6 +139,9 @@ def load() -> ctypes.CDLL:
         "oomb_qkv_project": [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp],
         "oomb_selftest_writeback_copy": [vp, i32, i32, i32],
         "oomb_qpage_lists": [vp, vp, vp, vp, i32, i32, vp, vp, vp, i32, vp],
+        "oomb_kv_append_rope": [vp, ctypes.POINTER(RopeArgs), vp],
+        "oomb_kv_append_rope_bwd": [vp, ctypes.POINTER(RopeArgs), vp],
+        "oomb_decode_attn": [vp, ctypes.POINTER(DecodeArgs), vp],
     }
     for name, args in sig.items():
         if not hasattr(lib, name):  # completeness is checked by the export test
@@ -133,6 +161,9 @@ def load() -> ctypes.CDLL:
     if hasattr(lib, "oomb_page_topk_batched_workspace_size"):
         lib.oomb_page_topk_batched_workspace_size.argtypes = [i32, i32, i32, i32]
         lib.oomb_page_topk_batched_workspace_size.restype = ctypes.c_size_t
+    if hasattr(lib, "oomb_decode_attn_workspace_size"):
+        lib.oomb_decode_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        lib.oomb_decode_attn_workspace_size.restype = ctypes.c_size_t
     lib.oomb_status_string.argtypes = [ctypes.c_int]
     lib.oomb_status_string.restype = ctypes.c_char_p
     lib.oomb_version.argtypes = []
@@ -162,6 +193,46 @@ def _dev_tensor(t, dtype, name):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Data pointer of a dense tensor of this type, shape (None: any) and device."""
+    if t.dtype != dtype or t.device != dev:
+        raise TypeError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
+    if t.dim() != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, n, heads, head_dim, dev, name):
+    """(data pointer, elements from row to row) of bf16 [n][heads][head_dim] whose
+    rows are dense but may stand apart, as the parts of a fused projection do."""
+    if t.dtype != torch.bfloat16 or t.device != dev:
+        raise TypeError(f"{name} must be {torch.bfloat16} on {dev}, got {t.dtype} on {t.device}")
+    if t.shape != (n, heads, head_dim):
+        raise ValueError(f"{name} must have the shape {(n, heads, head_dim)}, got "
+                         f"{tuple(t.shape)}")
+    row, head, one = t.stride()
+    if n <= 1:  # the distance of rows that are not there
+        row = heads * head_dim
+    if one != 1 or (head != head_dim and heads > 1):
+        raise ValueError(f"{name} must have dense rows [heads][head_dim]")
+    return t.data_ptr(), row
+
+
+def _stream_on(stream, dev):
+    """As _stream, but without one given the current stream of the tensors' device."""
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+
+
+def _pool_on(pool, t, name):
+    """The pool's descriptor; `t` must be on its device."""
+    d = pool_get_desc(pool)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != d.device:
+        raise TypeError(f"{name} must be a tensor on the pool's device (cuda:{d.device})")
+    return d
 
 
 # ------------------------------------------------------------------- pools
@@ -265,6 +336,92 @@ def kv_append(pool: int, page_ids: torch.Tensor, k: torch.Tensor, v: torch.Tenso
                                  _dev_tensor(k, torch.bfloat16, "k"),
                                  _dev_tensor(v, torch.bfloat16, "v"), _stream(stream)),
            "oomb_kv_append")
+
+
+def _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q, q_out,
+               interleaved, names):
+    d = _pool_on(pool, k, names[0])
+    dev, n, n_seqs = k.device, k.shape[0], cached_lens.numel()
+    H, D = d.num_kv_heads, d.head_dim
+    kp, ks = _rows(k, n, H, D, dev, names[0])
+    vp, vs = _rows(v, n, H, D, dev, names[1])
+    qp = qs = op = os_ = hq = 0
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{names[2]} and {names[3]} go together")
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _rows(q, n, hq, D, dev, names[2])
+        op, os_ = _rows(q_out, n, hq, D, dev, names[3])
+    i32 = torch.int32
+    return RopeArgs(
+        _arg(seq_start, i32, (n_seqs + 1,), dev, "seq_start"),
+        _arg(cached_lens, i32, (n_seqs,), dev, "cached_lens"),
+        _arg(page_tables, i32, (n_seqs, None), dev, "page_tables"),
+        _arg(positions, i32, (n,), dev, "positions"),
+        _arg(inv_freq, torch.float32, (None,), dev, "inv_freq"), kp, vp, qp, op, ks, vs, qs, os_,
+        n, n_seqs, page_tables.shape[1], hq, 2 * inv_freq.shape[0], bool(interleaved))
+
+
+def kv_append_rope(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q=None,
+                   q_out=None, interleaved=False, stream=None):
+    """oomb_kv_append_rope: k, v [n_tokens][Hkv][d] bf16 (rows may stand apart) of a
+    ragged batch, sequence b's tokens seq_start[b]:seq_start[b+1], into the pages
+    page_tables[b] from cache position cached_lens[b] on; keys, and queries q ->
+    q_out (which may be q), are rotated by positions * inv_freq ([rotary_dim / 2]
+    fp32).  Sets the page means and zeroes the new tokens' gradients."""
+    a = _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q, q_out,
+                   interleaved, ("k", "v", "q", "q_out"))
+    _check(load().oomb_kv_append_rope(pool, a, _stream_on(stream, k.device)),
+           "oomb_kv_append_rope")
+
+
+def kv_append_rope_bwd(pool, dk, dv, seq_start, cached_lens, page_tables, positions, inv_freq,
+                       dq=None, dq_out=None, interleaved=False, stream=None):
+    """oomb_kv_append_rope_bwd: the same tokens' gradients out of the gradient pool
+    into dk, dv (bf16, written; rows may stand apart), keys' rotated back, and dq
+    (of the rotated queries) -> dq_out rotated back (which may be dq)."""
+    a = _rope_args(pool, dk, dv, seq_start, cached_lens, page_tables, positions, inv_freq, dq,
+                   dq_out, interleaved, ("dk", "dv", "dq", "dq_out"))
+    _check(load().oomb_kv_append_rope_bwd(pool, a, _stream_on(stream, dk.device)),
+           "oomb_kv_append_rope_bwd")
+
+
+def decode_attn_workspace_size(n_seqs, num_q_heads, num_kv_heads, head_dim, n_groups=0) -> int:
+    """Bytes of decode_attn's workspace (uint8 tensor), on the current device."""
+    n = load().oomb_decode_attn_workspace_size(n_seqs, num_q_heads, num_kv_heads, head_dim,
+                                               n_groups)
+    if n == 0:
+        raise ValueError("decode_attn does not support these sizes")
+    return n
+
+
+def decode_attn(pool, q, o, page_tables, seq_lens, softmax_scale, workspace, lse=None,
+                prefix_pages=None, prefix_lens=None, group_start=None, stream=None):
+    """oomb_decode_attn: one query token per sequence (q, o [n_seqs][Hq][d] bf16, rows
+    may stand apart) over the first seq_lens[b] tokens of the pages page_tables[b]
+    and, with prefix_pages [n_groups][max_prefix_pages], prefix_lens [n_groups] and
+    group_start [n_groups + 1], over the prefix of the sequence's group, computed
+    once for the group.  lse: optional fp32 [n_seqs][Hq] output."""
+    d = _pool_on(pool, q, "q")
+    dev, i32 = q.device, torch.int32
+    n, hq, D = q.shape[0], q.shape[1], d.head_dim
+    qp, qs = _rows(q, n, hq, D, dev, "q")
+    op, os_ = _rows(o, n, hq, D, dev, "o")
+    lp = _arg(lse, torch.float32, (n, hq), dev, "lse") if lse is not None else None
+    ng = mp = 0
+    pp = pl = gs = None
+    if prefix_pages is not None or prefix_lens is not None or group_start is not None:
+        if prefix_pages is None or prefix_lens is None or group_start is None:
+            raise ValueError("prefix_pages, prefix_lens and group_start go together")
+        ng, mp = prefix_lens.numel(), prefix_pages.shape[-1]
+        pp = _arg(prefix_pages, i32, (ng, None), dev, "prefix_pages")
+        pl = _arg(prefix_lens, i32, (ng,), dev, "prefix_lens")
+        gs = _arg(group_start, i32, (ng + 1,), dev, "group_start")
+    a = DecodeArgs(qp, op, lp, qs, os_, _arg(page_tables, i32, (n, None), dev, "page_tables"),
+                   _arg(seq_lens, i32, (n,), dev, "seq_lens"), pp, pl, gs, n, hq,
+                   page_tables.shape[1], ng, mp, softmax_scale,
+                   _arg(workspace, torch.uint8, (None,), dev, "workspace"), workspace.numel())
+    _check(load().oomb_decode_attn(pool, a, _stream_on(stream, dev)), "oomb_decode_attn")
 
 
 def _attn_args(q, o, lse, past_pages, past_counts, cur_pages, softmax_scale, d_o=None, dq=None,
