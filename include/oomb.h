@@ -298,12 +298,13 @@ oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args,
  * O and the merge of the parts are fp32.  Results do not depend on what else
  * runs and are the same bits in every call on the same inputs.
  * Lengths and group starts are read on the device, so a captured graph replays
- * with new ones.  A length outside [0, max_pages * page_size] is clamped, a
- * group_start that decreases or leaves [0, n_seqs] is clamped to the previous
- * group's end or to n_seqs, both setting bit 2 of the device status word; a
+ * with new ones.  A length outside [0, max_pages * page_size] is clamped and
+ * sets bit 2 of the device status word, as does a group_start that decreases or
+ * leaves [0, n_seqs] (which prefix its sequences then see is not specified); a
  * page id outside the pool sets bit 0 and its tokens are skipped.
  * Requires a device pool, num_q_heads a multiple of num_kv_heads, softmax_scale
- * > 0, n_seqs <= 65535, n_groups <= n_seqs, rows of q and o dense [heads][head_dim],
+ * > 0, n_seqs <= 65535, n_seqs * num_q_heads < 2^31, n_groups <= n_seqs, max_pages
+ * (and, with groups, max_prefix_pages) >= 1, rows of q and o dense [heads][head_dim],
  * 16-byte aligned, *_stride elements apart (a multiple of 8).  o may be q.
  * The workspace (oomb_decode_attn_workspace_size() bytes, 16-byte aligned) needs
  * no initialisation; calls sharing one must be ordered (one stream).  n_seqs ==

@@ -1,9 +1,31 @@
 // decode_attn: one query token per sequence attends to the sequence's own pages
 // and to the pages of a prefix that it shares with others.
+//
+//   S_j = scale q.k_j,  m = max S_j,  l = sum e^(S_j - m),  O = sum e^(S_j - m) v_j / l
+//
+// over any split of the keys: parts (O_k, LSE_k) join as
+//   LSE = ln sum e^LSE_k,  O = sum e^(LSE_k - LSE) O_k.
+//
+// Three kernels, each a dependent launch of the one before:
+//   prefix_kernel (with prefix groups)  128 rows (sequence, head) of a group at
+//       once against the prefix's keys: its K and V are read once per 128 rows
+//       instead of once per sequence.  tcgen05, bound by the tensor cores and
+//       the exponentials for many rows, by memory for few.
+//   own_kernel   the up to 16 query heads of one KV head of one sequence against
+//       its own keys.  Each K and V value is used for G rows only: bound by
+//       memory, its matrix products are small (mma.sync m16n8k16, a fifth of
+//       that pipe's rate at the rate of HBM).
+//   merge_kernel joins the parts of a row.
+// The first two spread their work the same way: the key tiles of all units
+// (sequence or row tile, KV head) in a row are cut into equal ranges, one per
+// CTA, whatever the lengths are.  A unit that lies inside one range is whole;
+// of the others a CTA has at most two, the one it begins in and the one it ends
+// in, and writes them as parts into its two slots of the workspace.
 #include <algorithm>
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tmap.h"
 
 namespace {
 
@@ -11,6 +33,13 @@ using namespace oomb;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum moves when a tile's exceeds it by more than 2^8: sums and
+// products are rescaled rarely, and p <= 256 is as exact in bf16 as p <= 1.
+constexpr float kRescaleThreshold = 8.0f;
+
+constexpr int kOwnTile = 64;   // keys per tile of own_kernel
+constexpr int kOwnRows = 16;   // query rows of a unit of own_kernel
+constexpr int kPreTile = 128;  // keys, and rows, per tile of prefix_kernel
 
 struct DecodeParams {
   const __nv_bfloat16* q;
@@ -22,93 +51,1106 @@ struct DecodeParams {
   const int32_t* prefix_pages;
   const int32_t* prefix_lens;
   const int32_t* group_start;
-  const __nv_bfloat16* kv;
   uint32_t* status;
   int n_seqs, Hq, Hkv, G, P, max_pages, n_groups, max_prefix_pages, num_pages;
+  int row_tiles;  // units of kOwnRows query heads per KV head
   float scale_log2;
+  // Workspace.  Part results are normalised O (fp32) and base-2 LSE.
+  // own_meta [unit] {first CTA, CTAs}; slots [2 CTA + (0: begins before, 1: ends
+  // after this CTA)][rows]; rows [n_seqs Hq]: whole results that the merge joins
+  // with the other kernel's.
+  int2* own_meta;
+  float* own_slot_o;
+  float* own_slot_lse;
+  float* own_row_o;
+  float* own_row_lse;
+  int2* pre_meta;  // [n_seqs Hq]
+  float* pre_slot_o;
+  float* pre_slot_lse;
+  float* pre_row_o;
+  float* pre_row_lse;
 };
 
-// One CTA per (head, sequence): a warp takes a key at a time, a lane D / 32 of its values.
-template <int D>
-__global__ void __launch_bounds__(128) decode_kernel(const DecodeParams p) {
-  constexpr int E = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int h = blockIdx.x, b = blockIdx.y, g = h / p.G;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[b * p.q_stride + h * D + lane * E + e]);
-    acc[e] = 0.f;
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A length, clamped to what its page table holds.
+__device__ __forceinline__ int checked_len(int len, int max_pages, int P, uint32_t* status) {
+  const long long most = static_cast<long long>(max_pages) * P;
+  if (len >= 0 && len <= most) return len;
+  if (status) atomicOr(status, OOMB_DEV_BAD_COUNT);
+  return len < 0 ? 0 : static_cast<int>(most);
+}
+
+struct Group {
+  int lo, hi;  // its sequences
+  int len;     // its prefix
+};
+__device__ __forceinline__ Group group_of(const DecodeParams& p, int j, uint32_t* status) {
+  Group r;
+  const int lo = p.group_start[j], hi = p.group_start[j + 1];
+  r.lo = min(max(lo, 0), p.n_seqs);
+  r.hi = min(max(hi, r.lo), p.n_seqs);
+  if ((r.lo != lo || r.hi != hi) && status) atomicOr(status, OOMB_DEV_BAD_COUNT);
+  r.len = checked_len(p.prefix_lens[j], p.max_prefix_pages, p.P, status);
+  return r;
+}
+
+// Tiles of sequence b in own_kernel, all its units; an empty sequence has one
+// (all masked) per unit, which writes its result.
+__device__ __forceinline__ int own_tiles(int len) { return max(1, (len + kOwnTile - 1) / kOwnTile); }
+
+// The CTA's range [t0, t1) of a row of `total` tiles cut into equal parts, and
+// the item (of n items with weight(i) tiles each) in which t0 lies: all threads
+// sum weights of n / blockDim consecutive items each.
+struct Range {
+  long long total, per, t0, t1;
+  long long item_at;  // first tile of the item
+  int item;
+};
+template <int NT, class W>
+__device__ __forceinline__ Range find_range(int n, W weight) {
+  __shared__ long long warp_sum[NT / 32];
+  __shared__ Range sh;
+  const int t = threadIdx.x;
+  const int each = (n + NT - 1) / NT, i0 = min(n, t * each), i1 = min(n, i0 + each);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += weight(i, true);
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, d);
+    if ((t & 31) >= d) inc += v;
   }
-  int group = -1, at = 0;
-  for (int j = 0; j < p.n_groups; ++j) {
-    int lo = p.group_start[j], hi = p.group_start[j + 1];
-    if (lo < at || hi < lo || hi > p.n_seqs) {
-      if (threadIdx.x == 0) atomicOr(p.status, OOMB_DEV_BAD_COUNT);
-      lo = min(max(lo, at), p.n_seqs);
-      hi = min(max(hi, lo), p.n_seqs);
-    }
-    if (b >= lo && b < hi) group = j;
-    at = hi;
-  }
-  for (int part = 0; part < 2; ++part) {
-    if (part && group < 0) break;
-    const int cap = part ? p.max_prefix_pages : p.max_pages;
-    const int32_t* table =
-        part ? p.prefix_pages + static_cast<size_t>(group) * cap : p.page_tables + static_cast<size_t>(b) * cap;
-    int len = part ? p.prefix_lens[group] : p.seq_lens[b];
-    const long long most = static_cast<long long>(cap) * p.P;
-    if (len < 0 || len > most) {
-      if (threadIdx.x == 0) atomicOr(p.status, OOMB_DEV_BAD_COUNT);
-      len = len < 0 ? 0 : static_cast<int>(most);
-    }
-    for (int t = warp; t < len; t += 4) {
-      const int page = table[t / p.P];
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) atomicOr(p.status, OOMB_DEV_BAD_PAGE);
-        continue;
-      }
-      const __nv_bfloat16* kr =
-          p.kv + ((static_cast<size_t>(page) * p.Hkv + g) * 2 * p.P + t % p.P) * D + lane * E;
-      const __nv_bfloat16* vr = kr + static_cast<size_t>(p.P) * D;
-      float s = 0.f;
-      for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(kr[e]), s);
-      for (int o = 16; o; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= p.scale_log2;
-      const float m_new = fmaxf(m, s);
-      const float w = m_new == -INFINITY ? 0.f : fast_exp2(s - m_new);
-      const float c = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
-      l = l * c + w;
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * c + w * __bfloat162float(vr[e]);
-      m = m_new;
-    }
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+  if ((t & 31) == 31) warp_sum[t / 32] = inc;
   __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[w]);
-  float f[4];
-  for (int w = 0; w < 4; ++w) {
-    f[w] = sm[w] == -INFINITY ? 0.f : fast_exp2(sm[w] - top);
-    total += f[w] * sl[w];
+  long long before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < t / 32) before += warp_sum[w];
+    total += warp_sum[w];
   }
-  if (threadIdx.x < D) {
-    float o = 0.f;
-    for (int w = 0; w < 4; ++w) o += f[w] * so[w][threadIdx.x];
-    p.o[b * p.o_stride + h * D + threadIdx.x] =
-        __float2bfloat16(total > 0.f ? o / total : 0.f);
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long t0 = min(total, per * blockIdx.x), t1 = min(total, t0 + per);
+  if (t0 < t1 && before <= t0 && t0 < before + mine) {
+    int i = i0;
+    for (;; ++i) {
+      const long long w = weight(i, false);
+      if (t0 < before + w) break;
+      before += w;
+    }
+    sh.item = i;
+    sh.item_at = before;
   }
-  if (threadIdx.x == 0 && p.lse)
-    p.lse[static_cast<size_t>(b) * p.Hq + h] = total > 0.f ? kLn2 * (top + log2f(total)) : -INFINITY;
+  __syncthreads();
+  Range r = sh;
+  r.total = total;
+  r.per = per;
+  r.t0 = t0;
+  r.t1 = t1;
+  return r;
+}
+
+// ---------------------------------------------------------------- own keys
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+struct OwnCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kCtasPerSm = D == 128 ? 2 : 3;
+  static constexpr int kTileBytes = kOwnTile * D * 2 * 2;  // K and V
+  static constexpr int kQRow = D * 2 + 16;                 // padded: ldmatrix without bank conflicts
+  static constexpr int kQBytes = kOwnRows * kQRow;
+  static constexpr int kORow = D + 4;
+  static constexpr int kOBytes = 4 * kOwnRows * kORow * 4;
+  static constexpr int kSmem = kStages * (kTileBytes + kQBytes) + kOBytes + 1024;
+};
+
+// What the producer tells the consumers of a tile.
+struct TileInfo {
+  int unit;   // index of own_meta
+  int lim;    // valid keys of the tile, at most kOwnTile
+  int bad;    // bit w: the page of keys [16 w, 16 w + 16) is none
+  int flags;  // 1: first tile of the unit in this CTA, 2: last one, 4: whole unit, 8: it begins here
+};
+
+// Warps 0-3 take 16 keys of each tile (of one page: pages have 16 tokens or
+// more) and keep a maximum, a sum and an O of their own, so they meet only at
+// the end of a unit; warp 4 fills the ring of tiles by TMA (K and V of a page
+// and head are neighbours in the pool: one box of both per 64 columns).
+template <int D>
+__global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
+    own_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kvmap) {
+  using Cfg = OwnCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sq = ring + Cfg::kStages * Cfg::kTileBytes;
+  float* so = reinterpret_cast<float*>(sq + Cfg::kStages * Cfg::kQBytes);
+  __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages], bar_put, bar_got;
+  __shared__ TileInfo info[Cfg::kStages];
+  __shared__ float sm[4][kOwnRows], sl[4][kOwnRows];
+  __shared__ int abort_sh, issued_sh, used_sh;
+  const int warp = warp_id(), lane = lane_id();
+  volatile int* abort_flag = &abort_sh;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    abort_sh = issued_sh = used_sh = 0;
+    for (int i = 0; i < Cfg::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    mbar_init(&bar_put, 4);
+    mbar_init(&bar_got, 4);
+    fence_mbar_init();
+  }
+  const int units_per_seq = p.Hkv * p.row_tiles;
+  const Range rg = find_range<160>(p.n_seqs, [&](int b, bool note) {
+    const int len = checked_len(p.seq_lens[b], p.max_pages, p.P,
+                                note && blockIdx.x == 0 ? p.status : nullptr);
+    return static_cast<long long>(own_tiles(len)) * units_per_seq;
+  });
+  const int n_mine = static_cast<int>(rg.t1 - rg.t0);
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    const int R = min(p.P, kOwnTile);        // rows of a box
+    const int slots = kOwnTile / R;          // boxes of a tile, per 64 columns
+    const uint32_t box_bytes = 2u * R * 128;
+    const int lg_p = __ffs(p.P) - 1;
+    int b = rg.item, len = 0, nt = 1, tile = 0, u = 0, first_id = -1, ids = 0, issued = 0;
+    if (n_mine > 0) {
+      if (lane == 0) prefetch_tensormap(&kvmap);
+      len = checked_len(p.seq_lens[b], p.max_pages, p.P, nullptr);
+      nt = own_tiles(len);
+      const long long off = rg.t0 - rg.item_at;
+      u = static_cast<int>(off / nt);
+      tile = static_cast<int>(off - static_cast<long long>(u) * nt);
+    }
+    for (int i = 0; i < n_mine; ++i) {
+      const int st = i % Cfg::kStages;
+      const int g = u / p.row_tiles, rt = u % p.row_tiles;
+      const bool first = i == 0 || tile == 0, last = i == n_mine - 1 || tile == nt - 1;
+      const int key0 = tile * kOwnTile;
+      // 32 page ids at a time, one per lane
+      const int pg0 = key0 >> lg_p;
+      if (first_id < 0 || pg0 < first_id || pg0 + slots > first_id + 32) {
+        first_id = pg0;
+        const int at = pg0 + lane;
+        ids = at * static_cast<long long>(p.P) < len
+                  ? p.page_tables[static_cast<size_t>(b) * p.max_pages + at]
+                  : -1;
+      }
+      const int s = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;
+      int page = __shfl_sync(0xffffffffu, ids, (pg0 - first_id + s) & 31);
+      const int row0 = key0 + s * R;  // first token of the box
+      const bool here = s < slots && row0 < len;
+      const bool good = here && page >= 0 && page < p.num_pages;
+      const unsigned goods = __ballot_sync(0xffffffffu, good);
+      unsigned bad = 0;
+      for (int k = 0; k < 4; ++k) {  // keys [16 k, 16 k + 16)
+        const int l0 = (16 * k / R) * Cfg::kHalves;
+        if (key0 + 16 * k < len && !((goods >> l0) & 1u)) bad |= 1u << k;
+      }
+      if (here && !good && hf == 0 && u == 0) atomicOr(p.status, OOMB_DEV_BAD_PAGE);
+      const int rows = min(kOwnRows, p.G - rt * kOwnRows);
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, abort_flag);
+        if (ok) {
+          TileInfo t;
+          t.unit = b * units_per_seq + u;
+          t.lim = min(kOwnTile, len - key0);
+          t.bad = static_cast<int>(bad);
+          // the unit's first tile is this CTA's if it is not further back than its range
+          const bool begins = i >= tile, ends = tile == nt - 1;
+          t.flags = (first ? 1 : 0) | (last ? 2 : 0) | (begins && ends ? 4 : 0) | (begins ? 8 : 0);
+          info[st] = t;
+          mbar_arrive_expect_tx(&full[st], __popc(goods) * box_bytes + (first ? rows * D * 2 : 0));
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      ++issued;
+      if (first && lane < rows)
+        bulk_load(sq + st * Cfg::kQBytes + lane * Cfg::kQRow,
+                  p.q + b * p.q_stride + (g * p.G + rt * kOwnRows + lane) * D, D * 2, &full[st]);
+      if (good)
+        tma_load_4d(ring + st * Cfg::kTileBytes + (hf * slots + s) * box_bytes, &kvmap, &full[st],
+                    hf * 64, row0 & (p.P - 1), 2 * g, page);
+      if (first && tile == 0 && lane == 0) {
+        const int n = static_cast<int>((rg.t0 + i + nt - 1) / rg.per) - blockIdx.x + 1;
+        p.own_meta[b * units_per_seq + u] = make_int2(blockIdx.x, n);
+      }
+      // next tile
+      if (++tile == nt) {
+        tile = 0;
+        if (++u == units_per_seq) {
+          u = 0;
+          ++b;
+          first_id = -1;
+          if (i + 1 < n_mine) {
+            len = checked_len(p.seq_lens[b], p.max_pages, p.P, nullptr);
+            nt = own_tiles(len);
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      issued_sh = issued;
+      if (*abort_flag) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+    }
+  } else {
+    // ------------------------------------------------------------ consumers
+    const int R = min(p.P, kOwnTile), slots = kOwnTile / R;
+    // the 16 keys of this warp: slot and first row of it
+    const int my_slot = warp * 16 / R, my_row = warp * 16 % R;
+    const uint32_t box_bytes = 2u * R * 128;
+    const uint32_t ring_at = smem_u32(ring), sq_at = smem_u32(sq);
+    // ldmatrix rows: K: keys 0-7 / 8-15 x 8 columns, V (transposed) the same
+    const int kr = my_row + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+    const int vr = my_row + (lane & 15), vc = lane >> 4;
+    uint32_t qf[D / 16][4];
+    float acc[D / 8][4], m[2], l[2];
+    int used = 0, n_units = 0;
+    bool ok = true;
+    for (int i = 0; i < n_mine; ++i) {
+      const int st = i % Cfg::kStages;
+      if (!(ok = warp_wait(&full[st], (i / Cfg::kStages) & 1, abort_flag))) break;
+      ++used;
+      const TileInfo t = info[st];
+      if (t.flags & 1) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ldsm4(sq_at + st * Cfg::kQBytes + (lane & 15) * Cfg::kQRow + kk * 32 + (lane >> 4) * 16,
+                qf[kk]);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+      }
+      const int lim = t.lim - warp * 16;  // valid keys of this warp
+      if (lim > 0 && !((t.bad >> warp) & 1)) {
+        const uint32_t base = ring_at + st * Cfg::kTileBytes + my_slot * box_bytes;
+        float s[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t kb[4];
+          const uint32_t at = base + (kk / 4) * slots * box_bytes + kr * 128 +
+                              ((((kk % 4) * 2 + kc) ^ (kr & 7)) << 4);
+          ldsm4(at, kb);
+          mma16816(s[0], qf[kk], kb[0], kb[1]);
+          mma16816(s[1], qf[kk], kb[2], kb[3]);
+        }
+        // thread: rows lane / 4 and + 8, keys (lane % 4) 2 + {0, 1} and + 8
+        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+        if (lim < 16) {
+          const int k0 = (lane & 3) * 2;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (k0 + (e & 1) >= lim) s[0][e] = -INFINITY;
+            if (k0 + 8 + (e & 1) >= lim) s[1][e] = -INFINITY;
+          }
+          // values behind the end count 0 times, but 0 times NaN is NaN
+          vm0 = (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
+          vm1 = (k0 + 8 < lim ? 0xffffu : 0u) | (k0 + 9 < lim ? 0xffff0000u : 0u);
+        }
+        float mt[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          mt[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+          mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
+          mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2)) * p.scale_log2;
+        }
+        const bool need0 = mt[0] > m[0] + kRescaleThreshold, need1 = mt[1] > m[1] + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, need0 || need1)) {
+          const float a0 = need0 ? fast_exp2(m[0] - mt[0]) : 1.f;
+          const float a1 = need1 ? fast_exp2(m[1] - mt[1]) : 1.f;
+          if (need0) m[0] = mt[0];
+          if (need1) m[1] = mt[1];
+          l[0] *= a0;
+          l[1] *= a1;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            acc[c][0] *= a0;
+            acc[c][1] *= a0;
+            acc[c][2] *= a1;
+            acc[c][3] *= a1;
+          }
+        }
+        const float n0 = m[0] == -INFINITY ? 0.f : -m[0], n1 = m[1] == -INFINITY ? 0.f : -m[1];
+        uint32_t pa[4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float p0 = fast_exp2(fmaf(s[c][0], p.scale_log2, n0));
+          const float p1 = fast_exp2(fmaf(s[c][1], p.scale_log2, n0));
+          const float p2 = fast_exp2(fmaf(s[c][2], p.scale_log2, n1));
+          const float p3 = fast_exp2(fmaf(s[c][3], p.scale_log2, n1));
+          l[0] += p0 + p1;
+          l[1] += p2 + p3;
+          pa[2 * c] = pack_bf16(p0, p1);
+          pa[2 * c + 1] = pack_bf16(p2, p3);
+        }
+        const uint32_t vbase = base + R * 128 + vr * 128;
+#pragma unroll
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t vb[4];
+          ldsm4t(vbase + (cc / 4) * slots * box_bytes + ((((cc % 4) * 2 + vc) ^ (vr & 7)) << 4), vb);
+          if (lim < 16) {
+            vb[0] &= vm0;
+            vb[1] &= vm1;
+            vb[2] &= vm0;
+            vb[3] &= vm1;
+          }
+          mma16816(acc[2 * cc], pa, vb[0], vb[1]);
+          mma16816(acc[2 * cc + 1], pa, vb[2], vb[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (!(t.flags & 2)) continue;
+
+      // ---------------------------------------------------------- end of a unit
+      const int unit = t.unit, u = unit % units_per_seq, b = unit / units_per_seq;
+      const int h0 = (u / p.row_tiles) * p.G + (u % p.row_tiles) * kOwnRows;
+      const int rows = min(kOwnRows, p.G - (u % p.row_tiles) * kOwnRows);
+      // the last unit's sums have been read by all
+      if (n_units > 0 && !(ok = warp_wait(&bar_got, (n_units - 1) & 1, abort_flag))) break;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        const int row = lane / 4 + 8 * r;
+        if ((lane & 3) == 0) {
+          sm[warp][row] = m[r];
+          sl[warp][row] = l[r];
+        }
+        float* dst = so + (warp * kOwnRows + row) * Cfg::kORow + (lane & 3) * 2;
+        if (row < rows)
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<float2*>(dst + c * 8) = make_float2(acc[c][2 * r], acc[c][2 * r + 1]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_put);
+      if (!(ok = warp_wait(&bar_put, n_units & 1, abort_flag))) break;
+      ++n_units;
+      constexpr int TPR = D / 4, RPW = 32 / TPR;  // lanes of a row, rows of a warp
+      const bool whole = t.flags & 4;
+      const bool begins_before = !(t.flags & 8);
+      for (int row = warp * RPW + lane / TPR; row < rows; row += 4 * RPW) {
+        const int d4 = (lane % TPR) * 4;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[w][row]);
+        float total = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = sm[w][row] == -INFINITY ? 0.f : fast_exp2(sm[w][row] - top);
+          const float4 y = *reinterpret_cast<const float4*>(so + (w * kOwnRows + row) * Cfg::kORow + d4);
+          total = fmaf(f, sl[w][row], total);
+          x.x = fmaf(f, y.x, x.x);
+          x.y = fmaf(f, y.y, x.y);
+          x.z = fmaf(f, y.z, x.z);
+          x.w = fmaf(f, y.w, x.w);
+        }
+        const float inv = total > 0.f ? 1.f / total : 0.f;
+        const float lse2 = total > 0.f ? top + log2f(total) : -INFINITY;
+        x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        const size_t out_row = static_cast<size_t>(b) * p.Hq + h0 + row;
+        if (whole && p.n_groups == 0) {
+          *reinterpret_cast<uint2*>(p.o + b * p.o_stride + (h0 + row) * D + d4) =
+              make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+          if (d4 == 0 && p.lse) p.lse[out_row] = kLn2 * lse2;
+        } else {
+          const size_t slot_row =
+              (static_cast<size_t>(blockIdx.x) * 2 + (begins_before ? 0 : 1)) * kOwnRows + row;
+          float* od = whole ? p.own_row_o + out_row * D : p.own_slot_o + slot_row * D;
+          float* ld = whole ? p.own_row_lse + out_row : p.own_slot_lse + slot_row;
+          *reinterpret_cast<float4*>(od + d4) = x;
+          if (d4 == 0) *ld = lse2;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_got);
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+    }
+    if (warp == 0 && lane == 0) used_sh = used;
+  }
+  __syncthreads();
+  // after an abort, wait (bounded) for loads still landing in shared memory
+  if (abort_sh && threadIdx.x == 0)
+    for (int i = used_sh; i < issued_sh; ++i)
+      mbar_wait_drain(&full[i % Cfg::kStages], (i / Cfg::kStages) & 1);
+  __syncthreads();
+  pdl_wait();  // complete only after the kernel before: the merge waits for this one alone
+}
+
+// ---------------------------------------------------------------- shared prefixes
+template <int D>
+struct PreCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kPreTile * D * 2;  // K or V tile
+  static constexpr int kNK = 3;
+  static constexpr int kNV = 3;
+  static constexpr int kSmem = kTileBytes * (kNK + kNV) + 1024;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColO = 256;
+  static constexpr uint32_t kColQ = 384;
+};
+
+// Steps through the CTA's tiles: of unit u = (KV head, row tile) of group j.
+struct PreWalk {
+  Group gr;
+  int j, u, tile;
+  int nt, row_tiles;
+  __device__ __forceinline__ void load(const DecodeParams& p, uint32_t* status = nullptr) {
+    gr = group_of(p, j, status);
+    nt = (gr.len + kPreTile - 1) / kPreTile;
+    row_tiles = static_cast<int>(
+        (static_cast<long long>(gr.hi - gr.lo) * p.G + kPreTile - 1) / kPreTile);
+  }
+  __device__ __forceinline__ long long weight(const DecodeParams& p) const {
+    return static_cast<long long>(nt) * row_tiles * p.Hkv;
+  }
+  __device__ __forceinline__ void start(const DecodeParams& p, const Range& r) {
+    j = r.item;
+    load(p);
+    const long long off = r.t0 - r.item_at;
+    u = static_cast<int>(off / nt);
+    tile = static_cast<int>(off - static_cast<long long>(u) * nt);
+  }
+  __device__ __forceinline__ void next(const DecodeParams& p, bool more) {
+    if (++tile < nt) return;
+    tile = 0;
+    if (++u < row_tiles * p.Hkv) return;
+    u = 0;
+    if (!more) return;
+    do {
+      ++j;
+      load(p);
+    } while (weight(p) == 0);
+  }
+};
+
+// 128 rows (sequence, query head of the KV head) of a group against 128 keys a
+// tile.  Warps 0-3: thread r owns row r (TMEM lane r): its query goes to TMEM
+// once per unit, its scores come back from TMEM, p = 2^x goes to TMEM in their
+// place, O is rescaled when the maximum moves, and normalised at the end.  Warp 4
+// loads K tiles by TMA, warp 6 V tiles, warp 5 issues the products (S = Q K^T into
+// one of two buffers, O += P V).
+// TMEM columns: S0 [0,128), S1 [128,256), O [256,256+D), Q [384,384+D/2).
+template <int D>
+__global__ void __launch_bounds__(224, 1)
+    prefix_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kvmap) {
+  using Cfg = PreCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sK = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sV = sK + Cfg::kNK * Cfg::kTileBytes;
+  __shared__ uint64_t bar_qt, bar_drain, bar_o, bar_fin;
+  __shared__ uint64_t bar_kf[Cfg::kNK], bar_ke[Cfg::kNK], bar_vf[Cfg::kNV], bar_ve[Cfg::kNV];
+  __shared__ uint64_t bar_s[2], bar_p[2];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  __shared__ int k_issued_sh, v_issued_sh, k_used_sh, v_used_sh;
+  const int warp = warp_id(), lane = lane_id();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    abort_sh = 0;
+    k_issued_sh = v_issued_sh = k_used_sh = v_used_sh = 0;
+    mbar_init(&bar_qt, 4);
+    mbar_init(&bar_drain, 1);
+    mbar_init(&bar_o, 1);
+    mbar_init(&bar_fin, 1);
+    for (int i = 0; i < Cfg::kNK; ++i) {
+      mbar_init(&bar_kf[i], 1);
+      mbar_init(&bar_ke[i], 1);
+    }
+    for (int i = 0; i < Cfg::kNV; ++i) {
+      mbar_init(&bar_vf[i], 1);
+      mbar_init(&bar_ve[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_p[i], 4);
+    }
+    fence_mbar_init();
+  }
+  const Range rg = find_range<224>(p.n_groups, [&](int j, bool note) {
+    PreWalk w;
+    w.j = j;
+    w.load(p, note && blockIdx.x == 0 ? p.status : nullptr);
+    return w.weight(p);
+  });
+  if (rg.t0 >= rg.t1) return;  // the same for all threads of the CTA
+  const int n_mine = static_cast<int>(rg.t1 - rg.t0);
+  if (warp == 0) {
+    tmem_alloc(&tmem_base_sh, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort_flag = &abort_sh;
+  PreWalk w;
+  w.start(p, rg);
+  const int per = kPreTile / p.P;  // pages of a tile
+
+  if (warp == 4 || warp == 6) {
+    // ------------------------------------------------------------ producers
+    if (lane == 0) {
+      const bool is_k = warp == 4;
+      prefetch_tensormap(&kvmap);
+      const int nst = is_k ? Cfg::kNK : Cfg::kNV;
+      uint64_t* full = is_k ? bar_kf : bar_vf;
+      uint64_t* empty = is_k ? bar_ke : bar_ve;
+      uint8_t* base = is_k ? sK : sV;
+      int issued = 0;
+      for (int i = 0; i < n_mine; ++i) {
+        const int32_t* table = p.prefix_pages + static_cast<size_t>(w.j) * p.max_prefix_pages;
+        int pg[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const int li = w.tile * per + s;
+          // a page past the prefix, or one that is none: beyond the pool, filled with zeros
+          pg[s] = p.num_pages;
+          if (s < per && static_cast<long long>(li) * p.P < w.gr.len) {
+            const int id = table[li];
+            if (id >= 0 && id < p.num_pages) pg[s] = id;
+            else if (is_k) atomicOr(p.status, OOMB_DEV_BAD_PAGE);
+          }
+        }
+        const int g = w.u / w.row_tiles, st = i % nst;
+        if (!mbar_wait(&empty[st], ((i / nst) & 1) ^ 1, abort_flag)) break;
+        mbar_arrive_expect_tx(&full[st], Cfg::kTileBytes);
+        uint8_t* dst = base + st * Cfg::kTileBytes;
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < per)
+            for (int hf = 0; hf < Cfg::kHalves; ++hf)
+              tma_load_4d(dst + hf * kPreTile * 128 + s * p.P * 128, &kvmap, &full[st], hf * 64, 0,
+                          2 * g + (is_k ? 0 : 1), pg[s]);
+        ++issued;
+        w.next(p, i + 1 < n_mine);
+      }
+      if (*abort_flag) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+      if (is_k) k_issued_sh = issued;
+      else v_issued_sh = issued;
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+      const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV);
+      int k_used = 0, v_used = 0, n_units = 0;
+      bool ok = true, first = false, last = false;
+      // O += P V of tile i; `fst`: the first of its unit, `lst`: the last
+      auto pv = [&](int i, bool fst, bool lst) {
+        const int b = i & 1, vs = i % Cfg::kNV;
+        if (!mbar_wait(&bar_p[b], (i >> 1) & 1, abort_flag)) return false;
+        if (!mbar_wait(&bar_vf[vs], (i / Cfg::kNV) & 1, abort_flag)) return false;
+        ++v_used;
+        tc_fence_after();
+        const uint32_t vb = v_addr + vs * Cfg::kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < kPreTile / 16; ++kk)
+          umma_ts(tmem + Cfg::kColO, tmem + b * 128 + kk * 8,
+                  sw128_desc(vb + kk * 16 * 128, kPreTile * 128, 1024), idesc_pv,
+                  (!fst || kk > 0) ? 1u : 0u);
+        umma_commit(&bar_ve[vs]);
+        umma_commit(&bar_o);
+        if (lst) umma_commit(&bar_fin);
+        return true;
+      };
+      for (int i = 0; ok && i <= n_mine; ++i) {
+        const bool was_first = first, was_last = last;
+        bool done = i == 0;
+        if (i < n_mine) {
+          first = i == 0 || w.tile == 0;
+          last = i == n_mine - 1 || w.tile == w.nt - 1;
+          if (first) {
+            // the new unit's queries come when the old one's O has been read
+            if (!done && !(ok = pv(i - 1, was_first, was_last))) break;
+            done = true;
+            if (!(ok = mbar_wait(&bar_qt, n_units & 1, abort_flag))) break;
+            ++n_units;
+          }
+          const int ks = i % Cfg::kNK;
+          if (!(ok = mbar_wait(&bar_kf[ks], (i / Cfg::kNK) & 1, abort_flag))) break;
+          ++k_used;
+          tc_fence_after();
+          const uint32_t sd = tmem + (i & 1) * 128;
+          const uint32_t kb = k_addr + ks * Cfg::kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (kPreTile * 128) + (kk % 4) * 32;
+            umma_ts(sd, tmem + Cfg::kColQ + kk * 8, sw128_desc(kb + off, 16, 1024), idesc_s,
+                    kk > 0);
+          }
+          umma_commit(&bar_ke[ks]);
+          umma_commit(&bar_s[i & 1]);
+          w.next(p, i + 1 < n_mine);
+        }
+        if (!done) ok = pv(i - 1, was_first, was_last);
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+      }
+      // every product of this CTA has completed once bar_drain fires
+      umma_commit(&bar_drain);
+      mbar_wait_drain(&bar_drain, 0);
+      k_used_sh = k_used;
+      v_used_sh = v_used;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int r = threadIdx.x;  // 0..127
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    float m_used = -INFINITY, l = 0.f;
+    size_t out_row = 0;
+    int n_units = 0;
+    bool ok = true, valid = false, begins = false;
+    for (int i = 0; ok && i < n_mine; ++i) {
+      const int b = i & 1;
+      const bool first = i == 0 || w.tile == 0;
+      if (first) {
+        // this thread's row of the unit; its query into TMEM (A operand of S = Q K^T)
+        const int g = w.u / w.row_tiles, rt = w.u % w.row_tiles;
+        const long long rr = static_cast<long long>(rt) * kPreTile + r;
+        const int seq = w.gr.lo + static_cast<int>(rr / p.G), h = g * p.G + static_cast<int>(rr % p.G);
+        valid = seq < w.gr.hi;
+        begins = w.tile == 0;
+        out_row = static_cast<size_t>(seq) * p.Hq + h;
+        const __nv_bfloat16* qrow = p.q + seq * p.q_stride + h * D;
+#pragma unroll
+        for (int hf = 0; hf < Cfg::kHalves; ++hf) {
+          uint32_t qv[32];
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (valid) v = *reinterpret_cast<const uint4*>(qrow + hf * 64 + ch * 8);
+            qv[4 * ch] = v.x;
+            qv[4 * ch + 1] = v.y;
+            qv[4 * ch + 2] = v.z;
+            qv[4 * ch + 3] = v.w;
+          }
+          tmem_st32(tmem + lane_off + Cfg::kColQ + hf * 32, qv);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_qt);
+        if (valid && begins) {
+          const int n = static_cast<int>((rg.t0 + i + w.nt - 1) / rg.per) - blockIdx.x + 1;
+          p.pre_meta[out_row] = make_int2(blockIdx.x, n);
+        }
+        m_used = -INFINITY;
+        l = 0.f;
+      }
+      // a listed page that is none: its keys are masked (its tile holds zeros)
+      bool bad_page = false;
+      {
+        const int li = w.tile * per + lane;
+        if (lane < per && static_cast<long long>(li) * p.P < w.gr.len) {
+          const int id = p.prefix_pages[static_cast<size_t>(w.j) * p.max_prefix_pages + li];
+          bad_page = id < 0 || id >= p.num_pages;
+        }
+      }
+      if (!(ok = warp_wait(&bar_s[b], (i >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      float s[kPreTile];
+#pragma unroll
+      for (int c = 0; c < kPreTile / 32; ++c)
+        tmem_ld32(tmem + lane_off + b * 128 + c * 32, reinterpret_cast<uint32_t*>(s + c * 32));
+      tmem_ld_wait();
+      const int lim = w.gr.len - w.tile * kPreTile;
+      if (lim < kPreTile) {
+#pragma unroll
+        for (int c = 0; c < kPreTile; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+        // values behind the end count 0 times, but 0 times NaN is NaN: zero their rows
+        const int vs = i % Cfg::kNV;
+        if (!(ok = warp_wait(&bar_vf[vs], (i / Cfg::kNV) & 1, abort_flag))) break;
+        if (r >= lim) {
+#pragma unroll
+          for (int hf = 0; hf < Cfg::kHalves; ++hf) {
+            uint4* row = reinterpret_cast<uint4*>(sV + vs * Cfg::kTileBytes + hf * kPreTile * 128 +
+                                                  r * 128);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+      }
+      const uint32_t bad = __ballot_sync(0xffffffffu, bad_page);
+      if (bad) {
+        uint32_t drop = 0;
+        for (int k = 0; k < kPreTile / 16; ++k)
+          if ((bad >> (16 * k / p.P)) & 1u) drop |= 1u << k;
+#pragma unroll
+        for (int c = 0; c < kPreTile; ++c) s[c] = ((drop >> (c >> 4)) & 1u) ? -INFINITY : s[c];
+      }
+      float m8[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m8[e] = s[e];
+#pragma unroll
+      for (int c = 8; c < kPreTile; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
+      const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                             fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
+      const bool need = mt > m_used + kRescaleThreshold;
+      const float m_new = need ? mt : m_used;
+      const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
+      if (!first && __any_sync(0xffffffffu, need)) {
+        // PV of the tile before must land before O is rescaled.  S_i's commit implies
+        // that PV_{i-2} is complete and PV_i waits for P_i, so bar_o is in phase i-1
+        // or i here and the parity names PV_{i-1}.
+        if (!(ok = warp_wait(&bar_o, (i - 1) & 1, abort_flag))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + Cfg::kColO + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(tmem + lane_off + Cfg::kColO + c * 32, o);
+        }
+        tmem_st_wait();
+      }
+      m_used = m_new;
+      const float neg_mref = m_used == -INFINITY ? 0.f : -m_used;
+      float l8[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) l8[e] = 0.f;
+      uint32_t pk[kPreTile / 2];
+#pragma unroll
+      for (int c = 0; c < kPreTile / 2; ++c) {
+        const float p0 = fast_exp2(fmaf(s[2 * c], p.scale_log2, neg_mref));
+        const float p1 = fast_exp2(fmaf(s[2 * c + 1], p.scale_log2, neg_mref));
+        l8[c & 7] += p0 + p1;
+        pk[c] = pack_bf16(p0, p1);
+      }
+      l = l * alpha + (((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7])));
+#pragma unroll
+      for (int c = 0; c < kPreTile / 2 / 16; ++c)
+        tmem_st16(tmem + lane_off + b * 128 + c * 16, pk + c * 16);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_p[b]);
+
+      if (i == n_mine - 1 || w.tile == w.nt - 1) {
+        // ------------------------------------------------ end of a unit
+        if (!(ok = warp_wait(&bar_fin, n_units & 1, abort_flag))) break;
+        ++n_units;
+        tc_fence_after();
+        const bool whole = begins && w.tile == w.nt - 1;
+        const size_t slot_row = (static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * kPreTile + r;
+        float* od = whole ? p.pre_row_o + out_row * D : p.pre_slot_o + slot_row * D;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + Cfg::kColO + c * 32, o);
+          tmem_ld_wait();
+          if (valid)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(od + c * 32 + 4 * e) = make_float4(
+                  __uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                  __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+        }
+        if (valid)
+          *(whole ? p.pre_row_lse + out_row : p.pre_slot_lse + slot_row) =
+              l > 0.f ? m_used + log2f(l) : -INFINITY;
+        tc_fence_before();  // these reads come before the next unit's P and Q
+      }
+      w.next(p, i + 1 < n_mine);
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // After an abort, wait (bounded) for TMA loads still landing in shared memory.
+  if (abort_sh && warp == 4 && lane == 0) {
+    for (int i = k_used_sh; i < k_issued_sh; ++i)
+      mbar_wait_drain(&bar_kf[i % Cfg::kNK], (i / Cfg::kNK) & 1);
+    for (int i = v_used_sh; i < v_issued_sh; ++i)
+      mbar_wait_drain(&bar_vf[i % Cfg::kNV], (i / Cfg::kNV) & 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- merge
+// The group of sequence b: the last j with group_start[j] <= b, looked for by a
+// warp in steps of 32 (two round trips for up to 1024 groups); -1: none.
+__device__ __forceinline__ int find_group(const DecodeParams& p, int b) {
+  const int lane = lane_id();
+  int base = -1, n = p.n_groups + 1, from = 0;
+  while (n > 0) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const bool le = at < n && p.group_start[from + at] <= b;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    if (c == 0) break;
+    base = from + (c - 1) * step;
+    if (step == 1) break;
+    from = base;
+    n = min(step, n - (c - 1) * step);
+  }
+  return base >= 0 && base < p.n_groups ? base : -1;
+}
+
+// W warps per row (sequence, head); a lane takes 4 values of a part, a warp
+// 128 / D parts at once.
+template <int D, int W>
+__global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
+  constexpr int TPR = D / 4, PPW = 32 / TPR;
+  __shared__ float4 sx[4][TPR];
+  __shared__ float sm[4], sl[4];
+  const int warp = warp_id(), lane = lane_id();
+  const long long n_rows = static_cast<long long>(p.n_seqs) * p.Hq;
+  const long long row = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
+  const bool active = row < n_rows;
+  const int b = active ? static_cast<int>(row / p.Hq) : 0, h = active ? static_cast<int>(row % p.Hq) : 0;
+  int n_pre = 0, pre_row_in = 0;
+  if (p.n_groups > 0 && active) {
+    const int j = find_group(p, b);
+    if (j >= 0) {
+      const Group gr = group_of(p, j, nullptr);
+      if (b >= gr.lo && b < gr.hi && gr.len > 0) {
+        n_pre = 1;
+        pre_row_in = static_cast<int>(
+            (static_cast<long long>(b - gr.lo) * p.G + h % p.G) % kPreTile);
+      }
+    }
+  }
+  pdl_wait();
+  int2 own = make_int2(0, 0), pre = make_int2(0, 0);
+  if (active) {
+    own = p.own_meta[(static_cast<size_t>(b) * p.Hkv + h / p.G) * p.row_tiles + h % p.G / kOwnRows];
+    if (n_pre) pre = p.pre_meta[row];
+    // own_kernel has written this row already
+    if (p.n_groups == 0 && own.y == 1) own.y = -1;
+  }
+  const bool work = active && own.y >= 0;
+  const int n = work ? own.y + pre.y : 0;
+  const int own_row_in = h % p.G % kOwnRows;
+  auto lse_at = [&](int k) {
+    if (k < own.y) {
+      const size_t slot = static_cast<size_t>(own.x + k) * 2 + (k == 0);
+      return own.y == 1 ? p.own_row_lse + row : p.own_slot_lse + slot * kOwnRows + own_row_in;
+    }
+    k -= own.y;
+    const size_t slot = static_cast<size_t>(pre.x + k) * 2 + (k == 0);
+    return pre.y == 1 ? p.pre_row_lse + row : p.pre_slot_lse + slot * kPreTile + pre_row_in;
+  };
+  auto o_at = [&](int k) {
+    if (k < own.y) {
+      const size_t slot = static_cast<size_t>(own.x + k) * 2 + (k == 0);
+      return own.y == 1 ? p.own_row_o + row * D : p.own_slot_o + (slot * kOwnRows + own_row_in) * D;
+    }
+    k -= own.y;
+    const size_t slot = static_cast<size_t>(pre.x + k) * 2 + (k == 0);
+    return pre.y == 1 ? p.pre_row_o + row * D : p.pre_slot_o + (slot * kPreTile + pre_row_in) * D;
+  };
+  const int w = warp % W, sub = lane / TPR, d4 = (lane % TPR) * 4;
+  // the maximum over all parts, by every warp; then each warp its share of them
+  float top = -INFINITY;
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, *lse_at(k));
+#pragma unroll
+  for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+  if (top != -INFINITY) {
+#pragma unroll 4
+    for (int k = w * PPW + sub; k < n; k += W * PPW) {
+      const float f = fast_exp2(*lse_at(k) - top);
+      const float4 y = *reinterpret_cast<const float4*>(o_at(k) + d4);
+      total += f;
+      x.x = fmaf(f, y.x, x.x);
+      x.y = fmaf(f, y.y, x.y);
+      x.z = fmaf(f, y.z, x.z);
+      x.w = fmaf(f, y.w, x.w);
+    }
+  }
+#pragma unroll
+  for (int d = TPR; d < 32; d *= 2) {
+    total += __shfl_xor_sync(0xffffffffu, total, d);
+    x.x += __shfl_xor_sync(0xffffffffu, x.x, d);
+    x.y += __shfl_xor_sync(0xffffffffu, x.y, d);
+    x.z += __shfl_xor_sync(0xffffffffu, x.z, d);
+    x.w += __shfl_xor_sync(0xffffffffu, x.w, d);
+  }
+  if (W > 1) {
+    if (sub == 0) sx[warp][lane] = x;
+    if (lane == 0) sl[warp] = total;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int v = 1; v < W; ++v) {
+      const float4 y = sx[warp + v][lane % TPR];
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+      total += sl[warp + v];
+    }
+  }
+  if (!work || sub != 0) return;
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  *reinterpret_cast<uint2*>(p.o + b * p.o_stride + h * D + d4) =
+      make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+  if (lane == 0 && p.lse) p.lse[row] = total > 0.f ? kLn2 * (top + log2f(total)) : -INFINITY;
+}
+
+// ---------------------------------------------------------------- host
+int sm_count(int device) {
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = 148;
+  }
+  return n;
 }
 
 bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_groups) {
   return n_seqs >= 0 && n_seqs <= 65535 && Hkv > 0 && Hq > 0 && Hq % Hkv == 0 &&
-         supported_head_dim(D) && n_groups >= 0 && n_groups <= n_seqs;
+         supported_head_dim(D) && n_groups >= 0 && n_groups <= n_seqs &&
+         static_cast<int64_t>(n_seqs) * Hq <= INT32_MAX;
+}
+
+int own_ctas(int sms, int D) { return sms * (D == 128 ? OwnCfg<128>::kCtasPerSm : OwnCfg<64>::kCtasPerSm); }
+
+// Lays the workspace out from `base` (null: only counts) and returns its bytes.
+size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, int sms,
+               DecodeParams* p) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* r = base ? base + at : nullptr;
+    at += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  const size_t rows = static_cast<size_t>(n_seqs) * Hq;
+  const int row_tiles = (Hq / Hkv + kOwnRows - 1) / kOwnRows;
+  const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D)) * kOwnRows;
+  const size_t pre_rows = 2 * static_cast<size_t>(sms) * kPreTile;
+  p->own_meta = reinterpret_cast<int2*>(take(static_cast<size_t>(n_seqs) * Hkv * row_tiles * 8));
+  p->own_slot_o = reinterpret_cast<float*>(take(own_rows * D * 4));
+  p->own_slot_lse = reinterpret_cast<float*>(take(own_rows * 4));
+  p->own_row_o = p->own_row_lse = p->pre_slot_o = p->pre_slot_lse = p->pre_row_o = p->pre_row_lse =
+      nullptr;
+  p->pre_meta = nullptr;
+  if (n_groups > 0) {
+    p->own_row_o = reinterpret_cast<float*>(take(rows * D * 4));
+    p->own_row_lse = reinterpret_cast<float*>(take(rows * 4));
+    p->pre_meta = reinterpret_cast<int2*>(take(rows * 8));
+    p->pre_slot_o = reinterpret_cast<float*>(take(pre_rows * D * 4));
+    p->pre_slot_lse = reinterpret_cast<float*>(take(pre_rows * 4));
+    p->pre_row_o = reinterpret_cast<float*>(take(rows * D * 4));
+    p->pre_row_lse = reinterpret_cast<float*>(take(rows * 4));
+  }
+  return at;
+}
+
+// K and V boxes of `rows` tokens x 64 columns x `both` (1: K or V, 2: K and V).
+bool kv_map(CUtensorMap* map, const oomb_pool* pool, uint32_t rows, uint32_t both) {
+  const oomb_pool_desc& d = pool->desc;
+  const uint64_t D = d.head_dim, P = d.page_size, H2 = 2 * static_cast<uint64_t>(d.num_kv_heads);
+  const uint64_t dims[4] = {D, P, H2, static_cast<uint64_t>(d.num_pages)};
+  const uint64_t strides[3] = {D * 2, P * D * 2, H2 * P * D * 2};
+  const uint32_t box[4] = {64, rows, both, 1};
+  return make_bf16_map(map, pool->kv, 4, dims, strides, box);
+}
+
+template <int D>
+oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_done{0};
+  if (!once_per_device(attr_done, [] {
+        return cudaFuncSetAttribute(own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    OwnCfg<D>::kSmem) == cudaSuccess &&
+               cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    PreCfg<D>::kSmem) == cudaSuccess;
+      }))
+    return OOMB_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cudaError_t e = cudaSuccess;
+  CUtensorMap map;
+  if (p.n_groups > 0) {
+    if (!kv_map(&map, pool, p.P, 1)) return OOMB_ERR_CUDA;
+    cfg.gridDim = dim3(sms);
+    cfg.blockDim = dim3(224);
+    cfg.dynamicSmemBytes = PreCfg<D>::kSmem;
+    cfg.numAttrs = 0;
+    e = cudaLaunchKernelEx(&cfg, prefix_kernel<D>, p, map);
+  }
+  if (!kv_map(&map, pool, std::min(p.P, kOwnTile), 2)) return OOMB_ERR_CUDA;
+  if (e == cudaSuccess) {
+    cfg.gridDim = dim3(own_ctas(sms, D));
+    cfg.blockDim = dim3(160);
+    cfg.dynamicSmemBytes = OwnCfg<D>::kSmem;
+    cfg.numAttrs = p.n_groups > 0 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, own_kernel<D>, p, map);
+  }
+  if (e == cudaSuccess) {
+    const int64_t rows = static_cast<int64_t>(p.n_seqs) * p.Hq;
+    const bool wide = rows < 16 * static_cast<int64_t>(sms);
+    cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    e = wide ? cudaLaunchKernelEx(&cfg, merge_kernel<D, 4>, p)
+             : cudaLaunchKernelEx(&cfg, merge_kernel<D, 1>, p);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return OOMB_ERR_CUDA;
+  }
+  return check_launch();
 }
 
 }  // namespace
@@ -117,7 +1159,13 @@ extern "C" size_t oomb_decode_attn_workspace_size(int32_t n_seqs, int32_t num_q_
                                                   int32_t num_kv_heads, int32_t head_dim,
                                                   int32_t n_groups) {
   if (!good_shape(n_seqs, num_q_heads, num_kv_heads, head_dim, n_groups)) return 0;
-  return 256;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    dev = 0;
+  }
+  DecodeParams p;
+  return lay_out(nullptr, n_seqs, num_q_heads, num_kv_heads, head_dim, n_groups, sm_count(dev), &p);
 }
 
 extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args* a, void* stream) {
@@ -135,11 +1183,12 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   if (a->n_groups > 0 &&
       (a->max_prefix_pages <= 0 || !a->prefix_pages || !a->prefix_lens || !a->group_start))
     return OOMB_ERR_INVALID_ARG;
-  if (!a->workspace || !aligned16(a->workspace) ||
-      a->workspace_bytes <
-          oomb_decode_attn_workspace_size(a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups))
-    return OOMB_ERR_INVALID_ARG;
   DecodeParams p;
+  const int sms = sm_count(d.device);
+  if (!a->workspace || !aligned16(a->workspace) ||
+      a->workspace_bytes < lay_out(static_cast<uint8_t*>(a->workspace), a->n_seqs, Hq,
+                                   d.num_kv_heads, D, a->n_groups, sms, &p))
+    return OOMB_ERR_INVALID_ARG;
   p.q = static_cast<const __nv_bfloat16*>(a->q);
   p.o = static_cast<__nv_bfloat16*>(a->o);
   p.lse = a->lse;
@@ -150,7 +1199,6 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   p.prefix_pages = a->prefix_pages;
   p.prefix_lens = a->prefix_lens;
   p.group_start = a->group_start;
-  p.kv = static_cast<const __nv_bfloat16*>(pool->kv);
   p.status = pool->d_status;
   p.n_seqs = a->n_seqs;
   p.Hq = Hq;
@@ -161,11 +1209,9 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   p.n_groups = a->n_groups;
   p.max_prefix_pages = a->max_prefix_pages;
   p.num_pages = d.num_pages;
+  p.row_tiles = (p.G + kOwnRows - 1) / kOwnRows;
   p.scale_log2 = a->softmax_scale * kLog2e;
   DeviceGuard guard(d.device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(Hq, a->n_seqs);
-  if (D == 128) decode_kernel<128><<<grid, 128, 0, s>>>(p);
-  else decode_kernel<64><<<grid, 128, 0, s>>>(p);
-  return check_launch();
+  return D == 128 ? launch<128>(pool, p, sms, s) : launch<64>(pool, p, sms, s);
 }
