@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -139,9 +140,10 @@ def load() -> ctypes.CDLL:
         "oomb_qkv_project": [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp],
         "oomb_selftest_writeback_copy": [vp, i32, i32, i32],
         "oomb_qpage_lists": [vp, vp, vp, vp, i32, i32, vp, vp, vp, i32, vp],
-        "oomb_kv_append_rope": [vp, ctypes.POINTER(RopeArgs), vp],
-        "oomb_kv_append_rope_bwd": [vp, ctypes.POINTER(RopeArgs), vp],
-        "oomb_decode_attn": [vp, ctypes.POINTER(DecodeArgs), vp],
+        # oomb_rope_args / oomb_decode_args: a structure by reference, or its packed bytes
+        "oomb_kv_append_rope": [vp, vp, vp],
+        "oomb_kv_append_rope_bwd": [vp, vp, vp],
+        "oomb_decode_attn": [vp, vp, vp],
     }
     for name, args in sig.items():
         if not hasattr(lib, name):  # completeness is checked by the export test
@@ -196,42 +198,48 @@ def _dev_tensor(t, dtype, name):
 
 
 def _arg(t, dtype, shape, dev, name):
-    """Data pointer of a dense tensor of this type, shape (None: any) and device."""
-    if t.dtype != dtype or t.device != dev:
-        raise TypeError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
-    if t.dim() != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    """Data pointer of a dense tensor of this type, shape (None: any) and device index."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be {dtype} on cuda:{dev}, got {t.dtype} on {t.device}")
+    got = t.shape
+    if got != shape and (len(got) != len(shape) or
+                         any(n is not None and m != n for m, n in zip(got, shape))):
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(got)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, n, heads, head_dim, dev, name):
+def _rows(t, shape, dev, name):
     """(data pointer, elements from row to row) of bf16 [n][heads][head_dim] whose
     rows are dense but may stand apart, as the parts of a fused projection do."""
-    if t.dtype != torch.bfloat16 or t.device != dev:
-        raise TypeError(f"{name} must be {torch.bfloat16} on {dev}, got {t.dtype} on {t.device}")
-    if t.shape != (n, heads, head_dim):
-        raise ValueError(f"{name} must have the shape {(n, heads, head_dim)}, got "
-                         f"{tuple(t.shape)}")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        raise TypeError(f"{name} must be {torch.bfloat16} on cuda:{dev}, got {t.dtype} on "
+                        f"{t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
     row, head, one = t.stride()
-    if n <= 1:  # the distance of rows that are not there
-        row = heads * head_dim
-    if one != 1 or (head != head_dim and heads > 1):
+    if one != 1 or (head != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must have dense rows [heads][head_dim]")
+    if shape[0] <= 1:  # the distance of rows that are not there
+        row = shape[1] * shape[2]
     return t.data_ptr(), row
 
 
 def _stream_on(stream, dev):
     """As _stream, but without one given the current stream of the tensors' device."""
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _pool_on(pool, t, name):
-    """The pool's descriptor; `t` must be on its device."""
-    d = pool_get_desc(pool)
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != d.device:
+    """The pool's descriptor; `t` must be a tensor [rows][heads][head_dim] on its device."""
+    d = PoolDesc()
+    _check(load().oomb_pool_get_desc(pool, ctypes.byref(d)), "oomb_pool_get_desc")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != d.device:
         raise TypeError(f"{name} must be a tensor on the pool's device (cuda:{d.device})")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have the shape [rows][heads][head_dim], got "
+                         f"{tuple(t.shape)}")
     return d
 
 
@@ -338,28 +346,37 @@ def kv_append(pool: int, page_ids: torch.Tensor, k: torch.Tensor, v: torch.Tenso
            "oomb_kv_append")
 
 
+# oomb_rope_args and oomb_decode_args as packed bytes (the layout of RopeArgs and
+# DecodeArgs, which a test holds them to): a tenth of the time that filling a
+# ctypes structure takes, for calls made once per token.
+_ROPE_PACK = struct.Struct("@9P4q6i")
+_DECODE_PACK = struct.Struct("@3P2q5P5ifPN")
+
+
 def _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q, q_out,
                interleaved, names):
     d = _pool_on(pool, k, names[0])
-    dev, n, n_seqs = k.device, k.shape[0], cached_lens.numel()
-    H, D = d.num_kv_heads, d.head_dim
-    kp, ks = _rows(k, n, H, D, dev, names[0])
-    vp, vs = _rows(v, n, H, D, dev, names[1])
+    dev, n, n_seqs = d.device, k.shape[0], cached_lens.shape[0]
+    D = d.head_dim
+    shape = (n, d.num_kv_heads, D)
+    kp, ks = _rows(k, shape, dev, names[0])
+    vp, vs = _rows(v, shape, dev, names[1])
     qp = qs = op = os_ = hq = 0
-    if (q is None) != (q_out is None):
-        raise ValueError(f"{names[2]} and {names[3]} go together")
-    if q is not None:
+    if q is not None and q_out is not None:
         hq = q.shape[1]
-        qp, qs = _rows(q, n, hq, D, dev, names[2])
-        op, os_ = _rows(q_out, n, hq, D, dev, names[3])
-    i32 = torch.int32
-    return RopeArgs(
+        shape = (n, hq, D)
+        qp, qs = _rows(q, shape, dev, names[2])
+        op, os_ = _rows(q_out, shape, dev, names[3])
+    elif q is not None or q_out is not None:
+        raise ValueError(f"{names[2]} and {names[3]} go together")
+    i32, max_pages, half = torch.int32, page_tables.shape[-1], inv_freq.shape[0]
+    return dev, _ROPE_PACK.pack(
         _arg(seq_start, i32, (n_seqs + 1,), dev, "seq_start"),
         _arg(cached_lens, i32, (n_seqs,), dev, "cached_lens"),
-        _arg(page_tables, i32, (n_seqs, None), dev, "page_tables"),
+        _arg(page_tables, i32, (n_seqs, max_pages), dev, "page_tables"),
         _arg(positions, i32, (n,), dev, "positions"),
-        _arg(inv_freq, torch.float32, (None,), dev, "inv_freq"), kp, vp, qp, op, ks, vs, qs, os_,
-        n, n_seqs, page_tables.shape[1], hq, 2 * inv_freq.shape[0], bool(interleaved))
+        _arg(inv_freq, torch.float32, (half,), dev, "inv_freq"), kp, vp, qp, op, ks, vs, qs, os_,
+        n, n_seqs, max_pages, hq, 2 * half, bool(interleaved))
 
 
 def kv_append_rope(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q=None,
@@ -369,10 +386,9 @@ def kv_append_rope(pool, k, v, seq_start, cached_lens, page_tables, positions, i
     page_tables[b] from cache position cached_lens[b] on; keys, and queries q ->
     q_out (which may be q), are rotated by positions * inv_freq ([rotary_dim / 2]
     fp32).  Sets the page means and zeroes the new tokens' gradients."""
-    a = _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q, q_out,
-                   interleaved, ("k", "v", "q", "q_out"))
-    _check(load().oomb_kv_append_rope(pool, a, _stream_on(stream, k.device)),
-           "oomb_kv_append_rope")
+    dev, a = _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q,
+                        q_out, interleaved, ("k", "v", "q", "q_out"))
+    _check(load().oomb_kv_append_rope(pool, a, _stream_on(stream, dev)), "oomb_kv_append_rope")
 
 
 def kv_append_rope_bwd(pool, dk, dv, seq_start, cached_lens, page_tables, positions, inv_freq,
@@ -380,10 +396,9 @@ def kv_append_rope_bwd(pool, dk, dv, seq_start, cached_lens, page_tables, positi
     """oomb_kv_append_rope_bwd: the same tokens' gradients out of the gradient pool
     into dk, dv (bf16, written; rows may stand apart), keys' rotated back, and dq
     (of the rotated queries) -> dq_out rotated back (which may be dq)."""
-    a = _rope_args(pool, dk, dv, seq_start, cached_lens, page_tables, positions, inv_freq, dq,
-                   dq_out, interleaved, ("dk", "dv", "dq", "dq_out"))
-    _check(load().oomb_kv_append_rope_bwd(pool, a, _stream_on(stream, dk.device)),
-           "oomb_kv_append_rope_bwd")
+    dev, a = _rope_args(pool, dk, dv, seq_start, cached_lens, page_tables, positions, inv_freq, dq,
+                        dq_out, interleaved, ("dk", "dv", "dq", "dq_out"))
+    _check(load().oomb_kv_append_rope_bwd(pool, a, _stream_on(stream, dev)), "oomb_kv_append_rope_bwd")
 
 
 def decode_attn_workspace_size(n_seqs, num_q_heads, num_kv_heads, head_dim, n_groups=0) -> int:
@@ -403,24 +418,25 @@ def decode_attn(pool, q, o, page_tables, seq_lens, softmax_scale, workspace, lse
     group_start [n_groups + 1], over the prefix of the sequence's group, computed
     once for the group.  lse: optional fp32 [n_seqs][Hq] output."""
     d = _pool_on(pool, q, "q")
-    dev, i32 = q.device, torch.int32
-    n, hq, D = q.shape[0], q.shape[1], d.head_dim
-    qp, qs = _rows(q, n, hq, D, dev, "q")
-    op, os_ = _rows(o, n, hq, D, dev, "o")
-    lp = _arg(lse, torch.float32, (n, hq), dev, "lse") if lse is not None else None
-    ng = mp = 0
-    pp = pl = gs = None
+    dev, i32 = d.device, torch.int32
+    n, hq = q.shape[0], q.shape[1]
+    shape = (n, hq, d.head_dim)
+    qp, qs = _rows(q, shape, dev, "q")
+    op, os_ = _rows(o, shape, dev, "o")
+    lp = _arg(lse, torch.float32, (n, hq), dev, "lse") if lse is not None else 0
+    ng = mp = pp = pl = gs = 0
     if prefix_pages is not None or prefix_lens is not None or group_start is not None:
         if prefix_pages is None or prefix_lens is None or group_start is None:
             raise ValueError("prefix_pages, prefix_lens and group_start go together")
-        ng, mp = prefix_lens.numel(), prefix_pages.shape[-1]
-        pp = _arg(prefix_pages, i32, (ng, None), dev, "prefix_pages")
+        ng, mp = prefix_lens.shape[0], prefix_pages.shape[-1]
+        pp = _arg(prefix_pages, i32, (ng, mp), dev, "prefix_pages")
         pl = _arg(prefix_lens, i32, (ng,), dev, "prefix_lens")
         gs = _arg(group_start, i32, (ng + 1,), dev, "group_start")
-    a = DecodeArgs(qp, op, lp, qs, os_, _arg(page_tables, i32, (n, None), dev, "page_tables"),
-                   _arg(seq_lens, i32, (n,), dev, "seq_lens"), pp, pl, gs, n, hq,
-                   page_tables.shape[1], ng, mp, softmax_scale,
-                   _arg(workspace, torch.uint8, (None,), dev, "workspace"), workspace.numel())
+    max_pages, size = page_tables.shape[-1], workspace.shape[0]
+    a = _DECODE_PACK.pack(
+        qp, op, lp, qs, os_, _arg(page_tables, i32, (n, max_pages), dev, "page_tables"),
+        _arg(seq_lens, i32, (n,), dev, "seq_lens"), pp, pl, gs, n, hq, max_pages, ng, mp,
+        softmax_scale, _arg(workspace, torch.uint8, (size,), dev, "workspace"), size)
     _check(load().oomb_decode_attn(pool, a, _stream_on(stream, dev)), "oomb_decode_attn")
 
 

@@ -48,3 +48,11 @@ def test_workspace_size_of_refused_shapes_is_zero():
             pk.decode_attn_workspace_size(*bad)
     small, more = f(1, 28, 4, 128, 0), f(256, 28, 4, 128, 0)
     assert 0 < small <= more <= f(256, 28, 4, 128, 256)
+
+
+def test_packed_arguments_have_the_structures_layout():
+    for cls, pack in ((L.RopeArgs, L._ROPE_PACK), (L.DecodeArgs, L._DECODE_PACK)):
+        values = [i + 1 for i in range(len(cls._fields_))]
+        raw = cls.from_buffer_copy(pack.pack(*values).ljust(ctypes.sizeof(cls), b"\0"))
+        assert [getattr(raw, n) or 0 for n, _ in cls._fields_] == values
+        assert ctypes.sizeof(cls) - pack.size in (0, 4)  # padding behind the last field
