@@ -19,7 +19,7 @@ namespace {
 using namespace oomb;
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 8;  // tokens per CTA
+constexpr int kMaxTile = 32; // tokens per CTA
 constexpr int kMaxHalf = 64; // pairs of a head
 
 struct RopeParams {
@@ -40,6 +40,7 @@ struct RopeParams {
   int n_tokens, n_seqs, max_pages, Hq, Hkv, P, num_pages;
   int half;         // rotated pairs of a head
   int interleaved;
+  int lg_p;         // log2(P)
   int tile;         // tokens per CTA
 };
 
@@ -57,57 +58,65 @@ struct Places {
 };
 
 // Finds the sequence of each of the CTA's n <= 32 tokens: its index is the number
-// of starts <= t, less one.  All threads look through seq_start together (one
-// round trip for up to 256 sequences, where a binary search would take eight):
-// starts up to t0 are counted, those inside the tile marked.  `note`: report
-// what is wrong (one kernel of a call does).
-__device__ __forceinline__ void find_places(const RopeParams& p, int t0, int n, Places* out,
-                                            int* mark, bool note) {
+// of starts <= t, less one.  count_starts: all threads look through seq_start
+// together (one round trip for up to 256 sequences, where a binary search would
+// take eight): starts up to t0 are counted, those inside the tile marked.  After
+// a barrier, warp 0 looks the places up (find_places).  `note`: report what is
+// wrong (one kernel of a call does).
+__device__ __forceinline__ void count_starts(const RopeParams& p, int t0, int n, int first,
+                                             int* mark) {
   const int t = threadIdx.x;
   if (t < 32) mark[t] = 0;
   __syncthreads();
   int before = 0;
-  for (int i = t; i <= p.n_seqs; i += blockDim.x) {
-    const int s = p.seq_start[i];
+  for (int i = t, s = first; i <= p.n_seqs;) {
     if (s <= t0) ++before;
     else if (s < t0 + n) atomicAdd(&mark[s - t0], 1);
+    if ((i += kThreads) <= p.n_seqs) s = p.seq_start[i];
   }
-  if (before) atomicAdd(&mark[0], before);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (before && t % 32 == 0) atomicAdd(&mark[0], before);
   __syncthreads();
-  if (t < n) {
-    int seq = -1;
-    for (int j = 0; j <= t; ++j) seq += mark[j];
-    int page = -1, row = 0, last = 0, used = 0;
-    if (seq >= 0 && seq < p.n_seqs) {
-      const int tok = t0 + t, lo = p.seq_start[seq], hi = p.seq_start[seq + 1];
-      uint32_t bad = 0;
-      if (lo < 0 || tok < lo || tok >= hi || hi > p.n_tokens) {
-        bad = OOMB_DEV_BAD_COUNT;  // starts that decrease or leave the batch
+}
+__device__ __forceinline__ void find_places(const RopeParams& p, int t0, int n, Places* out,
+                                            const int* mark, bool note) {
+  const int t = threadIdx.x;  // < 32
+  int seq = mark[t];
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, seq, d);
+    if (t >= d) seq += v;
+  }
+  --seq;
+  int page = -1, row = 0, last = 0, used = 0;
+  if (t < n && seq >= 0 && seq < p.n_seqs) {
+    const int tok = t0 + t, lo = p.seq_start[seq], hi = p.seq_start[seq + 1];
+    const int cached = p.cached_lens[seq];
+    uint32_t bad = 0;
+    if (lo < 0 || tok < lo || tok >= hi || hi > p.n_tokens) {
+      bad = OOMB_DEV_BAD_COUNT;  // starts that decrease or leave the batch
+    } else {
+      used = 1;
+      const long long c = static_cast<long long>(cached) + (tok - lo);
+      const long long pi = c >> p.lg_p;
+      if (cached < 0 || pi >= p.max_pages) {
+        bad = OOMB_DEV_BAD_COUNT;
       } else {
-        used = 1;
-        const int cached = p.cached_lens[seq];
-        const long long c = static_cast<long long>(cached) + (tok - lo);
-        const long long pi = c / p.P;
-        if (cached < 0 || pi >= p.max_pages) {
-          bad = OOMB_DEV_BAD_COUNT;
-        } else {
-          row = static_cast<int>(c % p.P);
-          page = p.page_tables[static_cast<size_t>(seq) * p.max_pages + pi];
-          last = row == p.P - 1 || tok + 1 == hi;
-          if (page < 0 || page >= p.num_pages) {
-            bad = OOMB_DEV_BAD_PAGE;
-            page = -1;
-          }
+        row = static_cast<int>(c) & (p.P - 1);
+        page = p.page_tables[static_cast<size_t>(seq) * p.max_pages + pi];
+        last = row == p.P - 1 || tok + 1 == hi;
+        if (page < 0 || page >= p.num_pages) {
+          bad = OOMB_DEV_BAD_PAGE;
+          page = -1;
         }
       }
-      if (bad && note) atomicOr(p.status, bad);
     }
-    out->page[t] = page;
-    out->row[t] = row;
-    out->last[t] = last;
-    out->used[t] = used;
+    if (bad && note) atomicOr(p.status, bad);
   }
-  __syncthreads();
+  out->page[t] = page;
+  out->row[t] = row;
+  out->last[t] = last;
+  out->used[t] = used;
 }
 
 // cos and sin of pos * f, each rounded once to fp32.  pos * f has up to 55
@@ -140,102 +149,141 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
                     pack_bf16(x[6], x[7]));
 }
 
-// Unit u of a head: two 8-value vectors that are rotated (or copied) together.
-struct Unit {
-  int a, b;  // their first elements in the head
-  int f;     // first of their pairs, -1: not rotated
-};
-template <bool IL>
-__device__ __forceinline__ Unit unit_of(int u, int half, bool rotated) {
-  const bool turned = rotated && u < half / 8;
-  Unit r;
-  r.a = 16 * u;
-  r.b = r.a + 8;
-  r.f = turned ? 8 * u : -1;
-  if (!IL && turned) {
-    r.a = 8 * u;
-    r.b = r.a + half;
-  }
-  return r;
-}
-
-// Rotates the unit's values in place.  Products and sums are rounded one by
-// one (no contraction): what is stored is then the plain formula's value in
-// fp32, whichever of these kernels computes it.
+// Rotates eight pairs in place, of a lane's two 8-value vectors x and y of a
+// head: pair i = (x[i], y[i]), or neighbours in x (i < 4) and in y.  Products and
+// sums are rounded one by one (no contraction): what is stored is then the plain
+// formula's value in fp32.
 template <bool BACK, bool IL>
 __device__ __forceinline__ void rotate(float* x, float* y, const float* cs, const float* sn) {
-  float c[8], s[8];
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + i);
-    *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(sn + i);
-  }
+  for (int q = 0; q < 2; ++q) {
+    const float4 c4 = *reinterpret_cast<const float4*>(cs + 4 * q);
+    const float4 s4 = *reinterpret_cast<const float4*>(sn + 4 * q);
+    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (BACK) s[i] = -s[i];
-    // pair i of the unit: (x[i], y[i]), or neighbours in x (i < 4) and in y
-    float& pa = IL ? (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]) : x[i];
-    float& pb = IL ? (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]) : y[i];
-    const float a = pa, b = pb;
-    pa = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-    pb = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+    for (int e = 0; e < 4; ++e) {
+      const int i = 4 * q + e;
+      float& pa = IL ? (q == 0 ? x[2 * e] : y[2 * e]) : x[i];
+      float& pb = IL ? (q == 0 ? x[2 * e + 1] : y[2 * e + 1]) : y[i];
+      const float a = pa, b = pb;
+      const float bs = __fmul_rn(b, s[e]), as = __fmul_rn(a, s[e]);
+      pa = BACK ? __fadd_rn(__fmul_rn(a, c[e]), bs) : __fsub_rn(__fmul_rn(a, c[e]), bs);
+      pb = BACK ? __fsub_rn(__fmul_rn(b, c[e]), as) : __fadd_rn(__fmul_rn(b, c[e]), as);
+    }
   }
 }
 
-// One CTA: `tile` tokens, all their heads.  Heads are counted K, V, then Q; a
-// thread takes one unit (two 16-byte vectors) of one head of one token at a time.
+// One CTA: `tile` <= 32 tokens; 8 / tile warps for each, or each warp a token after
+// the other.  A warp takes the token's heads (counted K, V, then Q) 32 / (D / 16)
+// at a time.  A lane has the same two 16-byte vectors of each head, values [ea,
+// ea + 8) and [eb, eb + 8), chosen so that eight pairs lie in them; nothing is
+// divided per head.  The loads of a warp's first kBatch rounds are issued before
+// the angles and places are known.
 template <int D, bool BWD, bool IL>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  constexpr int UPH = D / 16;  // units per head
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
+  constexpr int UPH = D / 16;       // lanes per head
+  constexpr int HPP = 32 / UPH;     // heads of a warp at once
+  constexpr int kBatch = 3;
   __shared__ Places pl;
   __shared__ int mark[32];
   __shared__ __align__(16) float cs[kMaxTile * kMaxHalf], sn[kMaxTile * kMaxHalf];
   if (!BWD) pdl_launch_dependents();
   const int t0 = blockIdx.x * p.tile;
   const int n = min(p.tile, p.n_tokens - t0);
-  for (int i = threadIdx.x; i < n * p.half; i += kThreads)
-    turn(p.positions[t0 + i / p.half], p.inv_freq[i % p.half], cs + i, sn + i);
-  find_places(p, t0, n, &pl, mark, true);
-
-  const int heads = 2 * p.Hkv + p.Hq;
-  const int total = n * heads * UPH;
-  const size_t head_elems = static_cast<size_t>(p.P) * D;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < total; i += kThreads) {
-    const int u = i % UPH, h = (i / UPH) % heads, j = i / (UPH * heads);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int wpt = p.tile < 8 ? 8 / p.tile : 1;
+  const int j_from = warp / wpt, j_step = 8 / wpt;
+  const int u = lane % UPH;
+  const bool turned = u < p.half / 8;
+  const int ea = !IL && turned ? 8 * u : 16 * u;
+  const int eb = !IL && turned ? ea + p.half : ea + 8;
+  const int kv_heads = 2 * p.Hkv, heads = kv_heads + p.Hq;
+  const int h_mine = warp % wpt * HPP + lane / UPH, h_step = wpt * HPP;
+  const int h_from = (BWD ? kv_heads : 0) + h_mine;  // backward: queries first
+  uint4 xa[kBatch], xb[kBatch];
+  auto load = [&](int j, int h0) {
     const size_t tok = t0 + j;
-    const bool is_q = h >= 2 * p.Hkv, is_v = !is_q && h >= p.Hkv;
-    const int page = pl.page[j];
-    if (is_q ? !pl.used[j] : page < 0) continue;
-    const Unit un = unit_of<IL>(u, p.half, !is_v);
-    const int g = is_q ? h - 2 * p.Hkv : is_v ? h - p.Hkv : h;
-    // this head's row in the pool (K and V only)
-    const size_t at = is_q ? 0
-                           : ((static_cast<size_t>(page) * p.Hkv + g) * 2 + is_v) * head_elems +
-                                 static_cast<size_t>(pl.row[j]) * D;
-    __nv_bfloat16* tok_row = is_q ? nullptr
-                                  : (is_v ? p.v + tok * p.v_stride : p.k + tok * p.k_stride) + g * D;
-    float x[8], y[8];
-    if (BWD && !is_q) {
-      const float* src = p.grad + at;
+    const __nv_bfloat16* qrow = p.q + tok * p.q_stride - kv_heads * D;
+    const __nv_bfloat16* krow = p.k + tok * p.k_stride;
+    const __nv_bfloat16* vrow = p.v + tok * p.v_stride - p.Hkv * D;
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(src + un.a + e);
-        *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(src + un.b + e);
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * h_step;
+      if (h < heads) {
+        const __nv_bfloat16* src = (h >= kv_heads ? qrow : h >= p.Hkv ? vrow : krow) + h * D;
+        xa[i] = *reinterpret_cast<const uint4*>(src + ea);
+        xb[i] = *reinterpret_cast<const uint4*>(src + eb);
       }
-    } else {
-      const __nv_bfloat16* src = is_q ? p.q + tok * p.q_stride + g * D : tok_row;
-      unpack8(*reinterpret_cast<const uint4*>(src + un.a), x);
-      unpack8(*reinterpret_cast<const uint4*>(src + un.b), y);
     }
-    if (un.f >= 0) rotate<BWD, IL>(x, y, cs + j * p.half + un.f, sn + j * p.half + un.f);
-    __nv_bfloat16* dst = is_q ? p.q_out + tok * p.q_out_stride + g * D : BWD ? tok_row : p.kv + at;
-    *reinterpret_cast<uint4*>(dst + un.a) = pack8(x);
-    *reinterpret_cast<uint4*>(dst + un.b) = pack8(y);
-    if (!BWD && !is_q && p.grad) {
-      float4* gz = reinterpret_cast<float4*>(p.grad + at);
+  };
+  if (j_from < n) load(j_from, h_from);
+
+  count_starts(p, t0, n, threadIdx.x <= p.n_seqs ? p.seq_start[threadIdx.x] : 0, mark);
+  if (warp == 0) find_places(p, t0, n, &pl, mark, true);
+  else
+    for (int i = threadIdx.x - 32; i < n * p.half; i += kThreads - 32)
+      turn(p.positions[t0 + i / p.half], p.inv_freq[i % p.half], cs + i, sn + i);
+  __syncthreads();
+
+  const size_t head_elems = static_cast<size_t>(p.P) * D;
+  for (int j = j_from; j < n; j += j_step) {
+    const size_t tok = t0 + j;
+    const int page = pl.page[j];
+    const bool used = pl.used[j];
+    const float* cj = cs + j * p.half + 8 * u;
+    const float* sj = sn + j * p.half + 8 * u;
+    // the token's row of KV head 0's keys in the pool
+    const size_t pool_row = page < 0 ? 0
+                                     : static_cast<size_t>(page) * kv_heads * head_elems +
+                                           static_cast<size_t>(pl.row[j]) * D;
+    __nv_bfloat16* orow = p.q_out + tok * p.q_out_stride - kv_heads * D;
+    for (int h0 = h_from; h0 < heads; h0 += kBatch * h_step) {
+      if (j != j_from || h0 != h_from) load(j, h0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) gz[u + e * UPH] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * h_step;
+        if (h >= heads) break;
+        const bool is_q = h >= kv_heads, is_v = !is_q && h >= p.Hkv;
+        if (is_q ? !used : page < 0) continue;
+        // blocks of a page: K and V of KV head 0, of KV head 1, ...
+        const int block = is_v ? 2 * (h - p.Hkv) + 1 : 2 * h;
+        const size_t at = pool_row + block * head_elems;
+        __nv_bfloat16* dst = is_q ? orow + h * D : p.kv + at;
+        if (turned && !is_v) {
+          float x[8], y[8];
+          unpack8(xa[i], x);
+          unpack8(xb[i], y);
+          rotate<BWD, IL>(x, y, cj, sj);
+          xa[i] = pack8(x);
+          xb[i] = pack8(y);
+        }
+        *reinterpret_cast<uint4*>(dst + ea) = xa[i];
+        *reinterpret_cast<uint4*>(dst + eb) = xb[i];
+        if (!BWD && !is_q && p.grad) {
+          float4* gz = reinterpret_cast<float4*>(p.grad + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) gz[u + e * UPH] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    }
+    if (BWD && page >= 0) {
+      // the fp32 gradients of the token's keys and values
+#pragma unroll 2
+      for (int h = h_mine; h < kv_heads; h += h_step) {
+        const bool is_v = h >= p.Hkv;
+        const float* src = p.grad + pool_row + (is_v ? 2 * (h - p.Hkv) + 1 : 2 * h) * head_elems;
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(src + ea + e);
+          *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(src + eb + e);
+        }
+        if (turned && !is_v) rotate<BWD, IL>(x, y, cj, sj);
+        __nv_bfloat16* dst = is_v ? p.v + tok * p.v_stride + (h - p.Hkv) * D
+                                  : p.k + tok * p.k_stride + h * D;
+        *reinterpret_cast<uint4*>(dst + ea) = pack8(x);
+        *reinterpret_cast<uint4*>(dst + eb) = pack8(y);
+      }
     }
   }
 }
@@ -249,15 +297,18 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) page_mean_kernel(const RopeParams p) {
   constexpr int VPR = D / 8;      // 16-byte vectors per row
   constexpr int RPW = 32 / VPR;   // rows that a warp reads at once
+  constexpr int kBatch = 16;      // loads in flight per lane
   __shared__ Places pl;
   __shared__ int mark[32];
   const int t0 = blockIdx.x * p.tile;
   const int n = min(p.tile, p.n_tokens - t0);
-  find_places(p, t0, n, &pl, mark, false);
+  count_starts(p, t0, n, threadIdx.x <= p.n_seqs ? p.seq_start[threadIdx.x] : 0, mark);
+  if (threadIdx.x < 32) find_places(p, t0, n, &pl, mark, false);
+  __syncthreads();
   pdl_wait();  // the keys of this call are in the pages
   const int lane = threadIdx.x % 32, vec = lane % VPR, sub = lane / VPR;
-  const int g = blockIdx.y;
-  for (int j = threadIdx.x / 32; j < n; j += kThreads / 32) {
+  for (int i = threadIdx.x / 32; i < n * p.Hkv; i += kThreads / 32) {
+    const int j = i / p.Hkv, g = i % p.Hkv;
     if (!pl.last[j] || pl.page[j] < 0) continue;
     const size_t head = static_cast<size_t>(pl.page[j]) * p.Hkv + g;
     const __nv_bfloat16* src = p.kv + head * 2 * p.P * D + vec * 8;
@@ -265,13 +316,21 @@ __global__ void __launch_bounds__(kThreads) page_mean_kernel(const RopeParams p)
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-#pragma unroll 8
-    for (int r = sub; r < rows; r += RPW) {
-      float x[8];
-      unpack8(*reinterpret_cast<const uint4*>(src + static_cast<size_t>(r) * D), x);
+    for (int r0 = sub; r0 < rows; r0 += kBatch * RPW) {
+      uint4 v[kBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += x[e];
+      for (int b = 0; b < kBatch; ++b)
+        if (r0 + b * RPW < rows) v[b] = *reinterpret_cast<const uint4*>(src + (r0 + b * RPW) * D);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (r0 + b * RPW >= rows) break;
+        float x[8];
+        unpack8(v[b], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += x[e];
+      }
     }
+    __syncwarp();
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
 #pragma unroll
@@ -347,8 +406,10 @@ oomb_status make_params(const oomb_pool* pool, const oomb_rope_args* a, bool bwd
   p->num_pages = d.num_pages;
   p->half = a->rotary_dim / 2;
   p->interleaved = a->interleaved;
-  // about four CTAs per SM before a CTA takes more than one token
-  p->tile = std::min(kMaxTile, std::max(1, a->n_tokens / (4 * sm_count(d.device))));
+  p->lg_p = __builtin_ctz(static_cast<unsigned>(d.page_size));
+  // one wave of the four CTAs that an SM holds
+  const int slots = 4 * sm_count(d.device);
+  p->tile = std::min(kMaxTile, (a->n_tokens + slots - 1) / slots);
   return OOMB_OK;
 }
 
@@ -376,9 +437,9 @@ extern "C" oomb_status oomb_kv_append_rope(oomb_pool* pool, const oomb_rope_args
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   launch_rope<false>(p, d.head_dim, s);
   // page means: a dependent launch, its search for the pages runs beside the rotation
-  p.tile = std::min(32, std::max(1, p.n_tokens / (4 * sm_count(d.device))));
+  p.tile = std::min(32, std::max(1, p.n_tokens / sm_count(d.device)));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((p.n_tokens + p.tile - 1) / p.tile, d.num_kv_heads);
+  cfg.gridDim = dim3((p.n_tokens + p.tile - 1) / p.tile);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
