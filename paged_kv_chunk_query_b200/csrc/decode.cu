@@ -11,10 +11,9 @@
 //       once against the prefix's keys: its K and V are read once per 128 rows
 //       instead of once per sequence.  tcgen05, bound by the tensor cores and
 //       the exponentials for many rows, by memory for few.
-//   own_kernel   the up to 16 query heads of one KV head of one sequence against
-//       its own keys.  Each K and V value is used for G rows only: bound by
-//       memory, its matrix products are small (mma.sync m16n8k16, a fifth of
-//       that pipe's rate at the rate of HBM).
+//   own_kernel   8 or 16 query heads of one KV head of one sequence against its
+//       own keys.  Each K and V value is used for these few rows only: bound by
+//       memory, its matrix products are small (mma.sync m16n8k16).
 //   merge_kernel joins the parts of a row.
 // The first two spread their work the same way: the key tiles of all units
 // (sequence or row tile, KV head) in a row are cut into equal ranges, one per
@@ -38,7 +37,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;
 
 constexpr int kOwnTile = 64;   // keys per tile of own_kernel
-constexpr int kOwnRows = 16;   // query rows of a unit of own_kernel
 constexpr int kPreTile = 128;  // keys, and rows, per tile of prefix_kernel
 
 struct DecodeParams {
@@ -53,7 +51,8 @@ struct DecodeParams {
   const int32_t* group_start;
   uint32_t* status;
   int n_seqs, Hq, Hkv, G, P, max_pages, n_groups, max_prefix_pages, num_pages;
-  int row_tiles;  // units of kOwnRows query heads per KV head
+  int own_rows;   // query heads of a unit of own_kernel: 8 or 16
+  int row_tiles;  // its units per KV head
   float scale_log2;
   // Workspace.  Part results are normalised O (fp32) and base-2 LSE.
   // own_meta [unit] {first CTA, CTAs}; slots [2 CTA + (0: begins before, 1: ends
@@ -102,6 +101,14 @@ __device__ __forceinline__ Group group_of(const DecodeParams& p, int j, uint32_t
 // (all masked) per unit, which writes its result.
 __device__ __forceinline__ int own_tiles(int len) { return max(1, (len + kOwnTile - 1) / kOwnTile); }
 
+// Quotients of 64-bit numbers that nearly always fit 32 bits, where a division
+// takes a fifth of the time.
+__device__ __forceinline__ long long fast_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // The CTA's range [t0, t1) of a row of `total` tiles cut into equal parts, and
 // the item (of n items with weight(i) tiles each) in which t0 lies: all threads
 // sum weights of n / blockDim consecutive items each.
@@ -132,7 +139,7 @@ __device__ __forceinline__ Range find_range(int n, W weight) {
     if (w < t / 32) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long per = fast_div(total + gridDim.x - 1, gridDim.x);
   const long long t0 = min(total, per * blockIdx.x), t1 = min(total, t0 + per);
   if (t0 < t1 && before <= t0 && t0 < before + mine) {
     int i = i0;
@@ -166,43 +173,56 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
+// The transpose of an 8 x 8 matrix of 16-bit values spread over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+template <int D, int NT>
 struct OwnCfg {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kHalves = D / 64;
   static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kCtasPerSm = D == 128 ? 2 : 3;
   static constexpr int kTileBytes = kOwnTile * D * 2 * 2;  // K and V
   static constexpr int kQRow = D * 2 + 16;                 // padded: ldmatrix without bank conflicts
-  static constexpr int kQBytes = kOwnRows * kQRow;
+  static constexpr int kQBytes = kRows * kQRow;
   static constexpr int kORow = D + 4;
-  static constexpr int kOBytes = 4 * kOwnRows * kORow * 4;
+  static constexpr int kOBytes = 4 * kRows * kORow * 4;
   static constexpr int kSmem = kStages * (kTileBytes + kQBytes) + kOBytes + 1024;
 };
 
 // What the producer tells the consumers of a tile.
 struct TileInfo {
-  int unit;   // index of own_meta
   int lim;    // valid keys of the tile, at most kOwnTile
   int bad;    // bit w: the page of keys [16 w, 16 w + 16) is none
   int flags;  // 1: first tile of the unit in this CTA, 2: last one, 4: whole unit, 8: it begins here
+  int b, h0, rows;  // the unit: sequence, first query head, query heads
 };
 
+// The products are taken with the keys as the 16 rows of an m16n8k16: S^T = K Q^T
+// (16 keys x 8 heads), O^T += V^T P^T (16 of D x 8 heads).  With up to 8 heads per
+// KV head no row of an instruction is empty, and half the exponentials, registers
+// and instructions go that 16 rows of queries would take; more heads are NT = 2
+// such columns on the same K and V fragments.
 // Warps 0-3 take 16 keys of each tile (of one page: pages have 16 tokens or
 // more) and keep a maximum, a sum and an O of their own, so they meet only at
 // the end of a unit; warp 4 fills the ring of tiles by TMA (K and V of a page
 // and head are neighbours in the pool: one box of both per 64 columns).
-template <int D>
-__global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
+constexpr int kOwnThreads = 160;
+template <int D, int NT>
+__global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
     own_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kvmap) {
-  using Cfg = OwnCfg<D>;
+  using Cfg = OwnCfg<D, NT>;
+  constexpr int kRows = Cfg::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -210,11 +230,13 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
   float* so = reinterpret_cast<float*>(sq + Cfg::kStages * Cfg::kQBytes);
   __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages], bar_put, bar_got;
   __shared__ TileInfo info[Cfg::kStages];
-  __shared__ float sm[4][kOwnRows], sl[4][kOwnRows];
+  __shared__ float sm[4][kRows], sl[4][kRows];
   __shared__ int abort_sh, issued_sh, used_sh;
   const int warp = warp_id(), lane = lane_id();
   volatile int* abort_flag = &abort_sh;
+
   pdl_launch_dependents();
+  if (threadIdx.x == 128) prefetch_tensormap(&kvmap);
   if (threadIdx.x == 0) {
     abort_sh = issued_sh = used_sh = 0;
     for (int i = 0; i < Cfg::kStages; ++i) {
@@ -225,32 +247,51 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
     mbar_init(&bar_got, 4);
     fence_mbar_init();
   }
+  // heads past the unit's last stay zero: their scores would be NaN by chance
+  for (int i = threadIdx.x * 16; i < Cfg::kStages * Cfg::kQBytes; i += kOwnThreads * 16)
+    *reinterpret_cast<uint4*>(sq + i) = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
   const int units_per_seq = p.Hkv * p.row_tiles;
-  const Range rg = find_range<160>(p.n_seqs, [&](int b, bool note) {
+  const Range rg = find_range<kOwnThreads>(p.n_seqs, [&](int b, bool note) {
     const int len = checked_len(p.seq_lens[b], p.max_pages, p.P,
                                 note && blockIdx.x == 0 ? p.status : nullptr);
     return static_cast<long long>(own_tiles(len)) * units_per_seq;
   });
   const int n_mine = static_cast<int>(rg.t1 - rg.t0);
 
+
   if (warp == 4) {
     // ------------------------------------------------------------ producer
-    const int R = min(p.P, kOwnTile);        // rows of a box
-    const int slots = kOwnTile / R;          // boxes of a tile, per 64 columns
+    const int lg_p = __ffs(p.P) - 1, lg_r = min(lg_p, 6);
+    const int R = 1 << lg_r;                 // rows of a box
+    const int slots = kOwnTile >> lg_r;      // boxes of a tile, per 64 columns
     const uint32_t box_bytes = 2u * R * 128;
-    const int lg_p = __ffs(p.P) - 1;
-    int b = rg.item, len = 0, nt = 1, tile = 0, u = 0, first_id = -1, ids = 0, issued = 0;
+    const int s = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;  // this lane's box
+    const int per = static_cast<int>(rg.per);
+    int b = rg.item, len = 0, nt = 1, tile = 0, g = 0, rt = 0, first_id = -1, ids = 0, issued = 0;
+    // the next sequence's length and first page ids, under way while this one's tiles are
+    int next_len = 0, next_ids = -1;
+    auto look_ahead = [&] {
+      if (b + 1 < p.n_seqs) {
+        next_len = p.seq_lens[b + 1];
+        if (lane < p.max_pages)
+          next_ids = p.page_tables[static_cast<size_t>(b + 1) * p.max_pages + lane];
+      }
+    };
+    int2* meta = p.own_meta;  // of the current unit
     if (n_mine > 0) {
-      if (lane == 0) prefetch_tensormap(&kvmap);
       len = checked_len(p.seq_lens[b], p.max_pages, p.P, nullptr);
+      look_ahead();
       nt = own_tiles(len);
       const long long off = rg.t0 - rg.item_at;
-      u = static_cast<int>(off / nt);
+      const int u = static_cast<int>(fast_div(off, nt));
       tile = static_cast<int>(off - static_cast<long long>(u) * nt);
+      g = u / p.row_tiles;
+      rt = u - g * p.row_tiles;
+      meta += static_cast<size_t>(b) * units_per_seq + u;
     }
     for (int i = 0; i < n_mine; ++i) {
       const int st = i % Cfg::kStages;
-      const int g = u / p.row_tiles, rt = u % p.row_tiles;
       const bool first = i == 0 || tile == 0, last = i == n_mine - 1 || tile == nt - 1;
       const int key0 = tile * kOwnTile;
       // 32 page ids at a time, one per lane
@@ -262,30 +303,32 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
                   ? p.page_tables[static_cast<size_t>(b) * p.max_pages + at]
                   : -1;
       }
-      const int s = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;
-      int page = __shfl_sync(0xffffffffu, ids, (pg0 - first_id + s) & 31);
-      const int row0 = key0 + s * R;  // first token of the box
+      const int page = __shfl_sync(0xffffffffu, ids, (pg0 - first_id + s) & 31);
+      const int row0 = key0 + (s << lg_r);  // first token of the box
       const bool here = s < slots && row0 < len;
       const bool good = here && page >= 0 && page < p.num_pages;
       const unsigned goods = __ballot_sync(0xffffffffu, good);
       unsigned bad = 0;
-      for (int k = 0; k < 4; ++k) {  // keys [16 k, 16 k + 16)
-        const int l0 = (16 * k / R) * Cfg::kHalves;
-        if (key0 + 16 * k < len && !((goods >> l0) & 1u)) bad |= 1u << k;
+      if (goods != __ballot_sync(0xffffffffu, here)) {
+        for (int k = 0; k < 4; ++k)  // keys [16 k, 16 k + 16)
+          if (key0 + 16 * k < len && !((goods >> (((16 * k) >> lg_r) * Cfg::kHalves)) & 1u))
+            bad |= 1u << k;
+        if (here && !good && hf == 0 && g == 0 && rt == 0) atomicOr(p.status, OOMB_DEV_BAD_PAGE);
       }
-      if (here && !good && hf == 0 && u == 0) atomicOr(p.status, OOMB_DEV_BAD_PAGE);
-      const int rows = min(kOwnRows, p.G - rt * kOwnRows);
+      const int h0 = g * p.G + rt * kRows, rows = min(kRows, p.G - rt * kRows);
       bool ok = true;
       if (lane == 0) {
         ok = mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, abort_flag);
         if (ok) {
-          TileInfo t;
-          t.unit = b * units_per_seq + u;
-          t.lim = min(kOwnTile, len - key0);
-          t.bad = static_cast<int>(bad);
           // the unit's first tile is this CTA's if it is not further back than its range
           const bool begins = i >= tile, ends = tile == nt - 1;
+          TileInfo t;
+          t.lim = min(kOwnTile, len - key0);
+          t.bad = static_cast<int>(bad);
           t.flags = (first ? 1 : 0) | (last ? 2 : 0) | (begins && ends ? 4 : 0) | (begins ? 8 : 0);
+          t.b = b;
+          t.h0 = h0;
+          t.rows = rows;
           info[st] = t;
           mbar_arrive_expect_tx(&full[st], __popc(goods) * box_bytes + (first ? rows * D * 2 : 0));
         }
@@ -293,27 +336,32 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       ++issued;
-      if (first && lane < rows)
-        bulk_load(sq + st * Cfg::kQBytes + lane * Cfg::kQRow,
-                  p.q + b * p.q_stride + (g * p.G + rt * kOwnRows + lane) * D, D * 2, &full[st]);
       if (good)
         tma_load_4d(ring + st * Cfg::kTileBytes + (hf * slots + s) * box_bytes, &kvmap, &full[st],
                     hf * 64, row0 & (p.P - 1), 2 * g, page);
-      if (first && tile == 0 && lane == 0) {
-        const int n = static_cast<int>((rg.t0 + i + nt - 1) / rg.per) - blockIdx.x + 1;
-        p.own_meta[b * units_per_seq + u] = make_int2(blockIdx.x, n);
+      if (first && lane < rows)
+        bulk_load(sq + st * Cfg::kQBytes + lane * Cfg::kQRow,
+                  p.q + b * p.q_stride + (h0 + lane) * D, D * 2, &full[st]);
+      if (tile == 0 && lane == 0) {
+        const int over = nt - (n_mine - i);  // its tiles in later CTAs
+        *meta = make_int2(blockIdx.x, over <= 0 ? 1 : 1 + (over + per - 1) / per);
       }
       // next tile
       if (++tile == nt) {
         tile = 0;
-        if (++u == units_per_seq) {
-          u = 0;
+        ++meta;
+        if (++rt == p.row_tiles) {
+          rt = 0;
+          ++g;
+        }
+        if (g == p.Hkv) {
+          g = 0;
           ++b;
-          first_id = -1;
-          if (i + 1 < n_mine) {
-            len = checked_len(p.seq_lens[b], p.max_pages, p.P, nullptr);
-            nt = own_tiles(len);
-          }
+          len = checked_len(next_len, p.max_pages, p.P, nullptr);
+          nt = own_tiles(len);
+          first_id = 0;
+          ids = next_ids;
+          look_ahead();
         }
       }
     }
@@ -323,16 +371,17 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
     }
   } else {
     // ------------------------------------------------------------ consumers
-    const int R = min(p.P, kOwnTile), slots = kOwnTile / R;
+    const int lg_r = min(__ffs(p.P) - 1, 6), R = 1 << lg_r, slots = kOwnTile >> lg_r;
     // the 16 keys of this warp: slot and first row of it
-    const int my_slot = warp * 16 / R, my_row = warp * 16 % R;
+    const int my_slot = (warp * 16) >> lg_r, my_row = (warp * 16) & (R - 1);
     const uint32_t box_bytes = 2u * R * 128;
     const uint32_t ring_at = smem_u32(ring), sq_at = smem_u32(sq);
-    // ldmatrix rows: K: keys 0-7 / 8-15 x 8 columns, V (transposed) the same
-    const int kr = my_row + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
-    const int vr = my_row + (lane & 15), vc = lane >> 4;
-    uint32_t qf[D / 16][4];
-    float acc[D / 8][4], m[2], l[2];
+    // ldmatrix addresses: K (keys 0-15, two chunks of 8 columns), V transposed (two
+    // chunks of 8 columns, keys 0-7 and 8-15)
+    const int kr = my_row + (lane & 15), kc = lane >> 4;
+    const int vr = my_row + (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+    uint32_t qf[NT][D / 16][2];
+    float acc[NT][D / 16][4], m[NT][2], l[NT][2];
     int used = 0, n_units = 0;
     bool ok = true;
     for (int i = 0; i < n_mine; ++i) {
@@ -342,93 +391,105 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
       const TileInfo t = info[st];
       if (t.flags & 1) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          ldsm4(sq_at + st * Cfg::kQBytes + (lane & 15) * Cfg::kQRow + kk * 32 + (lane >> 4) * 16,
-                qf[kk]);
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
+          for (int kk = 0; kk < D / 16; kk += 2)
+            ldsm4(sq_at + st * Cfg::kQBytes + (n * 8 + (lane & 7)) * Cfg::kQRow + kk * 32 +
+                      (lane >> 3) * 16,
+                  qf[n][kk]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][c][e] = 0.f;
+          m[n][0] = m[n][1] = -INFINITY;
+          l[n][0] = l[n][1] = 0.f;
+        }
       }
       const int lim = t.lim - warp * 16;  // valid keys of this warp
       if (lim > 0 && !((t.bad >> warp) & 1)) {
         const uint32_t base = ring_at + st * Cfg::kTileBytes + my_slot * box_bytes;
-        float s[2][4];
+        // thread: keys lane / 4 and + 8, heads (lane % 4) 2 + {0, 1}; two chains of products
+        float s[NT][4], s2[NT][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           uint32_t kb[4];
-          const uint32_t at = base + (kk / 4) * slots * box_bytes + kr * 128 +
-                              ((((kk % 4) * 2 + kc) ^ (kr & 7)) << 4);
-          ldsm4(at, kb);
-          mma16816(s[0], qf[kk], kb[0], kb[1]);
-          mma16816(s[1], qf[kk], kb[2], kb[3]);
-        }
-        // thread: rows lane / 4 and + 8, keys (lane % 4) 2 + {0, 1} and + 8
-        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
-        if (lim < 16) {
-          const int k0 = (lane & 3) * 2;
+          ldsm4(base + (kk / 4) * slots * box_bytes + kr * 128 +
+                    ((((kk % 4) * 2 + kc) ^ (kr & 7)) << 4),
+                kb);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (k0 + (e & 1) >= lim) s[0][e] = -INFINITY;
-            if (k0 + 8 + (e & 1) >= lim) s[1][e] = -INFINITY;
-          }
+          for (int n = 0; n < NT; ++n)
+            mma16816(kk & 1 ? s2[n] : s[n], kb, qf[n][kk][0], qf[n][kk][1]);
+        }
+        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+        const bool ragged = lim < 16;
+        if (ragged) {
           // values behind the end count 0 times, but 0 times NaN is NaN
+          const int k0 = (lane & 3) * 2;
           vm0 = (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
           vm1 = (k0 + 8 < lim ? 0xffffu : 0u) | (k0 + 9 < lim ? 0xffff0000u : 0u);
         }
-        float mt[2];
+        bool need = false;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          mt[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-          mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
-          mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2)) * p.scale_log2;
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[n][e] = (s[n][e] + s2[n][e]) * p.scale_log2;
+            if (ragged && lane / 4 + (e >> 1) * 8 >= lim) s[n][e] = -INFINITY;
+          }
+          need |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kRescaleThreshold ||
+                  fmaxf(s[n][1], s[n][3]) > m[n][1] + kRescaleThreshold;
         }
-        const bool need0 = mt[0] > m[0] + kRescaleThreshold, need1 = mt[1] > m[1] + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, need0 || need1)) {
-          const float a0 = need0 ? fast_exp2(m[0] - mt[0]) : 1.f;
-          const float a1 = need1 ? fast_exp2(m[1] - mt[1]) : 1.f;
-          if (need0) m[0] = mt[0];
-          if (need1) m[1] = mt[1];
-          l[0] *= a0;
-          l[1] *= a1;
+        // the maximum over the keys is only taken when one of them is too far above it
+        if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            acc[c][0] *= a0;
-            acc[c][1] *= a0;
-            acc[c][2] *= a1;
-            acc[c][3] *= a1;
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mt = fmaxf(s[n][e], s[n][e + 2]);
+              mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+              mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+              mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+              if (mt <= m[n][e]) continue;
+              const float a = fast_exp2(m[n][e] - mt);
+              m[n][e] = mt;
+              l[n][e] *= a;
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                acc[n][c][e] *= a;
+                acc[n][c][e + 2] *= a;
+              }
+            }
           }
         }
-        const float n0 = m[0] == -INFINITY ? 0.f : -m[0], n1 = m[1] == -INFINITY ? 0.f : -m[1];
-        uint32_t pa[4];
+        uint32_t pb[NT][2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float p0 = fast_exp2(fmaf(s[c][0], p.scale_log2, n0));
-          const float p1 = fast_exp2(fmaf(s[c][1], p.scale_log2, n0));
-          const float p2 = fast_exp2(fmaf(s[c][2], p.scale_log2, n1));
-          const float p3 = fast_exp2(fmaf(s[c][3], p.scale_log2, n1));
-          l[0] += p0 + p1;
-          l[1] += p2 + p3;
-          pa[2 * c] = pack_bf16(p0, p1);
-          pa[2 * c + 1] = pack_bf16(p2, p3);
+        for (int n = 0; n < NT; ++n) {
+          const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+          const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+          const float p0 = fast_exp2(s[n][0] - m0), p1 = fast_exp2(s[n][1] - m1);
+          const float p2 = fast_exp2(s[n][2] - m0), p3 = fast_exp2(s[n][3] - m1);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          pb[n][0] = transpose8(pack_bf16(p0, p1));
+          pb[n][1] = transpose8(pack_bf16(p2, p3));
         }
         const uint32_t vbase = base + R * 128 + vr * 128;
 #pragma unroll
-        for (int cc = 0; cc < D / 16; ++cc) {
-          uint32_t vb[4];
-          ldsm4t(vbase + (cc / 4) * slots * box_bytes + ((((cc % 4) * 2 + vc) ^ (vr & 7)) << 4), vb);
-          if (lim < 16) {
-            vb[0] &= vm0;
-            vb[1] &= vm1;
-            vb[2] &= vm0;
-            vb[3] &= vm1;
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t va[4];
+          ldsm4t(vbase + (c / 4) * slots * box_bytes + ((((c % 4) * 2 + vc) ^ (vr & 7)) << 4), va);
+          if (ragged) {
+            va[0] &= vm0;
+            va[1] &= vm0;
+            va[2] &= vm1;
+            va[3] &= vm1;
           }
-          mma16816(acc[2 * cc], pa, vb[0], vb[1]);
-          mma16816(acc[2 * cc + 1], pa, vb[2], vb[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(acc[n][c], va, pb[n][0], pb[n][1]);
         }
       }
       __syncwarp();
@@ -436,25 +497,30 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
       if (!(t.flags & 2)) continue;
 
       // ---------------------------------------------------------- end of a unit
-      const int unit = t.unit, u = unit % units_per_seq, b = unit / units_per_seq;
-      const int h0 = (u / p.row_tiles) * p.G + (u % p.row_tiles) * kOwnRows;
-      const int rows = min(kOwnRows, p.G - (u % p.row_tiles) * kOwnRows);
+      const int b = t.b, h0 = t.h0, rows = t.rows;
       // the last unit's sums have been read by all
       if (n_units > 0 && !(ok = warp_wait(&bar_got, (n_units - 1) & 1, abort_flag))) break;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        const int row = lane / 4 + 8 * r;
-        if ((lane & 3) == 0) {
-          sm[warp][row] = m[r];
-          sl[warp][row] = l[r];
-        }
-        float* dst = so + (warp * kOwnRows + row) * Cfg::kORow + (lane & 3) * 2;
-        if (row < rows)
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            *reinterpret_cast<float2*>(dst + c * 8) = make_float2(acc[c][2 * r], acc[c][2 * r + 1]);
+        for (int e = 0; e < 2; ++e) {
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+          const int row = n * 8 + (lane & 3) * 2 + e;
+          if (lane < 4) {
+            sm[warp][row] = m[n][e];
+            sl[warp][row] = l[n][e];
+          }
+          // O^T of head `row`: 16 c + lane / 4 and + 8
+          if (m[n][e] == -INFINITY) continue;  // no keys here: not read
+          float* dst = so + (warp * kRows + row) * Cfg::kORow + lane / 4;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            dst[16 * c] = acc[n][c][e];
+            dst[16 * c + 8] = acc[n][c][e + 2];
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_put);
@@ -463,38 +529,52 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
       constexpr int TPR = D / 4, RPW = 32 / TPR;  // lanes of a row, rows of a warp
       const bool whole = t.flags & 4;
       const bool begins_before = !(t.flags & 8);
-      for (int row = warp * RPW + lane / TPR; row < rows; row += 4 * RPW) {
-        const int d4 = (lane % TPR) * 4;
-        float top = -INFINITY;
+      const int d4 = (lane % TPR) * 4;
+      // two rows at a time, so that their chains overlap
+      for (int row0 = warp * RPW + lane / TPR; row0 < rows; row0 += 8 * RPW) {
+        float top[2], total[2], mw[2][4];
+        float4 x[2];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[w][row]);
-        float total = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < 2; ++k) {
+          const int row = min(row0 + k * 4 * RPW, kRows - 1);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float f = sm[w][row] == -INFINITY ? 0.f : fast_exp2(sm[w][row] - top);
-          const float4 y = *reinterpret_cast<const float4*>(so + (w * kOwnRows + row) * Cfg::kORow + d4);
-          total = fmaf(f, sl[w][row], total);
-          x.x = fmaf(f, y.x, x.x);
-          x.y = fmaf(f, y.y, x.y);
-          x.z = fmaf(f, y.z, x.z);
-          x.w = fmaf(f, y.w, x.w);
+          for (int w = 0; w < 4; ++w) mw[k][w] = sm[w][row];
+          top[k] = fmaxf(fmaxf(mw[k][0], mw[k][1]), fmaxf(mw[k][2], mw[k][3]));
+          total[k] = 0.f;
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            if (mw[k][w] == -INFINITY) continue;  // a warp that had no keys
+            const float f = fast_exp2(mw[k][w] - top[k]);
+            const float4 y =
+                *reinterpret_cast<const float4*>(so + (w * kRows + row) * Cfg::kORow + d4);
+            total[k] = fmaf(f, sl[w][row], total[k]);
+            x[k].x = fmaf(f, y.x, x[k].x);
+            x[k].y = fmaf(f, y.y, x[k].y);
+            x[k].z = fmaf(f, y.z, x[k].z);
+            x[k].w = fmaf(f, y.w, x[k].w);
+          }
         }
-        const float inv = total > 0.f ? 1.f / total : 0.f;
-        const float lse2 = total > 0.f ? top + log2f(total) : -INFINITY;
-        x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-        const size_t out_row = static_cast<size_t>(b) * p.Hq + h0 + row;
-        if (whole && p.n_groups == 0) {
-          *reinterpret_cast<uint2*>(p.o + b * p.o_stride + (h0 + row) * D + d4) =
-              make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-          if (d4 == 0 && p.lse) p.lse[out_row] = kLn2 * lse2;
-        } else {
-          const size_t slot_row =
-              (static_cast<size_t>(blockIdx.x) * 2 + (begins_before ? 0 : 1)) * kOwnRows + row;
-          float* od = whole ? p.own_row_o + out_row * D : p.own_slot_o + slot_row * D;
-          float* ld = whole ? p.own_row_lse + out_row : p.own_slot_lse + slot_row;
-          *reinterpret_cast<float4*>(od + d4) = x;
-          if (d4 == 0) *ld = lse2;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int row = row0 + k * 4 * RPW;
+          if (row >= rows) break;
+          const float inv = total[k] > 0.f ? 1.f / total[k] : 0.f;
+          const float lse2 = total[k] > 0.f ? top[k] + log2f(total[k]) : -INFINITY;
+          const float4 y = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
+          const size_t out_row = static_cast<size_t>(b) * p.Hq + h0 + row;
+          if (whole && p.n_groups == 0) {
+            *reinterpret_cast<uint2*>(p.o + b * p.o_stride + (h0 + row) * D + d4) =
+                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+            if (d4 == 0 && p.lse) p.lse[out_row] = kLn2 * lse2;
+          } else {
+            const size_t slot_row =
+                (static_cast<size_t>(blockIdx.x) * 2 + (begins_before ? 0 : 1)) * kRows + row;
+            float* od = whole ? p.own_row_o + out_row * D : p.own_slot_o + slot_row * D;
+            float* ld = whole ? p.own_row_lse + out_row : p.own_slot_lse + slot_row;
+            *reinterpret_cast<float4*>(od + d4) = y;
+            if (d4 == 0) *ld = lse2;
+          }
         }
       }
       __syncwarp();
@@ -512,6 +592,7 @@ __global__ void __launch_bounds__(160, OwnCfg<D>::kCtasPerSm)
     for (int i = used_sh; i < issued_sh; ++i)
       mbar_wait_drain(&full[i % Cfg::kStages], (i / Cfg::kStages) & 1);
   __syncthreads();
+
   pdl_wait();  // complete only after the kernel before: the merge waits for this one alone
 }
 
@@ -546,7 +627,7 @@ struct PreWalk {
     j = r.item;
     load(p);
     const long long off = r.t0 - r.item_at;
-    u = static_cast<int>(off / nt);
+    u = static_cast<int>(fast_div(off, nt));
     tile = static_cast<int>(off - static_cast<long long>(u) * nt);
   }
   __device__ __forceinline__ void next(const DecodeParams& p, bool more) {
@@ -967,18 +1048,18 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
   pdl_wait();
   int2 own = make_int2(0, 0), pre = make_int2(0, 0);
   if (active) {
-    own = p.own_meta[(static_cast<size_t>(b) * p.Hkv + h / p.G) * p.row_tiles + h % p.G / kOwnRows];
+    own = p.own_meta[(static_cast<size_t>(b) * p.Hkv + h / p.G) * p.row_tiles + h % p.G / p.own_rows];
     if (n_pre) pre = p.pre_meta[row];
     // own_kernel has written this row already
     if (p.n_groups == 0 && own.y == 1) own.y = -1;
   }
   const bool work = active && own.y >= 0;
   const int n = work ? own.y + pre.y : 0;
-  const int own_row_in = h % p.G % kOwnRows;
+  const int own_row_in = h % p.G % p.own_rows;
   auto lse_at = [&](int k) {
     if (k < own.y) {
       const size_t slot = static_cast<size_t>(own.x + k) * 2 + (k == 0);
-      return own.y == 1 ? p.own_row_lse + row : p.own_slot_lse + slot * kOwnRows + own_row_in;
+      return own.y == 1 ? p.own_row_lse + row : p.own_slot_lse + slot * p.own_rows + own_row_in;
     }
     k -= own.y;
     const size_t slot = static_cast<size_t>(pre.x + k) * 2 + (k == 0);
@@ -987,54 +1068,79 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
   auto o_at = [&](int k) {
     if (k < own.y) {
       const size_t slot = static_cast<size_t>(own.x + k) * 2 + (k == 0);
-      return own.y == 1 ? p.own_row_o + row * D : p.own_slot_o + (slot * kOwnRows + own_row_in) * D;
+      return own.y == 1 ? p.own_row_o + row * D : p.own_slot_o + (slot * p.own_rows + own_row_in) * D;
     }
     k -= own.y;
     const size_t slot = static_cast<size_t>(pre.x + k) * 2 + (k == 0);
     return pre.y == 1 ? p.pre_row_o + row * D : p.pre_slot_o + (slot * kPreTile + pre_row_in) * D;
   };
   const int w = warp % W, sub = lane / TPR, d4 = (lane % TPR) * 4;
-  // the maximum over all parts, by every warp; then each warp its share of them
-  float top = -INFINITY;
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, *lse_at(k));
-#pragma unroll
-  for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  // each warp (or part of one) its share of the parts, four loads of LSE and O at
+  // once: a running maximum instead of a pass over the LSEs first, which would be one
+  // more round trip
+  float top = -INFINITY, total = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  float total = 0.f;
-  if (top != -INFINITY) {
-#pragma unroll 4
-    for (int k = w * PPW + sub; k < n; k += W * PPW) {
-      const float f = fast_exp2(*lse_at(k) - top);
-      const float4 y = *reinterpret_cast<const float4*>(o_at(k) + d4);
+  constexpr int kBatch = 4;
+  for (int k0 = w * PPW + sub; k0 < n; k0 += kBatch * W * PPW) {
+    float lk[kBatch];
+    float4 y[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = k0 + i * W * PPW;
+      lk[i] = -INFINITY;
+      if (k < n) {
+        lk[i] = *lse_at(k);
+        y[i] = *reinterpret_cast<const float4*>(o_at(k) + d4);
+      }
+    }
+    const float m = fmaxf(fmaxf(fmaxf(lk[0], lk[1]), fmaxf(lk[2], lk[3])), top);
+    if (m == -INFINITY) continue;
+    const float c = fast_exp2(top - m);
+    top = m;
+    total *= c;
+    x = make_float4(x.x * c, x.y * c, x.z * c, x.w * c);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (lk[i] == -INFINITY) continue;  // no such part, or one without keys
+      const float f = fast_exp2(lk[i] - m);
       total += f;
-      x.x = fmaf(f, y.x, x.x);
-      x.y = fmaf(f, y.y, x.y);
-      x.z = fmaf(f, y.z, x.z);
-      x.w = fmaf(f, y.w, x.w);
+      x.x = fmaf(f, y[i].x, x.x);
+      x.y = fmaf(f, y[i].y, x.y);
+      x.z = fmaf(f, y[i].z, x.z);
+      x.w = fmaf(f, y[i].w, x.w);
     }
   }
+  __syncwarp();
+  auto join = [&](float t2, float l2, float4 y) {
+    const float m = fmaxf(top, t2);
+    if (m == -INFINITY) return;
+    const float f = fast_exp2(top - m), f2 = fast_exp2(t2 - m);
+    top = m;
+    total = total * f + l2 * f2;
+    x = make_float4(x.x * f + y.x * f2, x.y * f + y.y * f2, x.z * f + y.z * f2,
+                    x.w * f + y.w * f2);
+  };
 #pragma unroll
   for (int d = TPR; d < 32; d *= 2) {
-    total += __shfl_xor_sync(0xffffffffu, total, d);
-    x.x += __shfl_xor_sync(0xffffffffu, x.x, d);
-    x.y += __shfl_xor_sync(0xffffffffu, x.y, d);
-    x.z += __shfl_xor_sync(0xffffffffu, x.z, d);
-    x.w += __shfl_xor_sync(0xffffffffu, x.w, d);
+    float4 y;
+    y.x = __shfl_xor_sync(0xffffffffu, x.x, d);
+    y.y = __shfl_xor_sync(0xffffffffu, x.y, d);
+    y.z = __shfl_xor_sync(0xffffffffu, x.z, d);
+    y.w = __shfl_xor_sync(0xffffffffu, x.w, d);
+    const float t2 = __shfl_xor_sync(0xffffffffu, top, d);
+    const float l2 = __shfl_xor_sync(0xffffffffu, total, d);
+    join(t2, l2, y);
   }
   if (W > 1) {
     if (sub == 0) sx[warp][lane] = x;
-    if (lane == 0) sl[warp] = total;
+    if (lane == 0) {
+      sm[warp] = top;
+      sl[warp] = total;
+    }
     __syncthreads();
     if (w != 0) return;
 #pragma unroll
-    for (int v = 1; v < W; ++v) {
-      const float4 y = sx[warp + v][lane % TPR];
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
-      total += sl[warp + v];
-    }
+    for (int v = 1; v < W; ++v) join(sm[warp + v], sl[warp + v], sx[warp + v][lane % TPR]);
   }
   if (!work || sub != 0) return;
   const float inv = total > 0.f ? 1.f / total : 0.f;
@@ -1059,7 +1165,11 @@ bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_gr
          static_cast<int64_t>(n_seqs) * Hq <= INT32_MAX;
 }
 
-int own_ctas(int sms, int D) { return sms * (D == 128 ? OwnCfg<128>::kCtasPerSm : OwnCfg<64>::kCtasPerSm); }
+int own_ctas(int sms, int D) {
+  return sms * (D == 128 ? OwnCfg<128, 1>::kCtasPerSm : OwnCfg<64, 1>::kCtasPerSm);
+}
+// Query heads of a unit of own_kernel: one column of 8, or two.
+int own_unit_rows(int G) { return G <= 8 ? 8 : 16; }
 
 // Lays the workspace out from `base` (null: only counts) and returns its bytes.
 size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, int sms,
@@ -1071,10 +1181,12 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
     return r;
   };
   const size_t rows = static_cast<size_t>(n_seqs) * Hq;
-  const int row_tiles = (Hq / Hkv + kOwnRows - 1) / kOwnRows;
-  const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D)) * kOwnRows;
+  const int G = Hq / Hkv;
+  p->own_rows = own_unit_rows(G);
+  p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
+  const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D)) * p->own_rows;
   const size_t pre_rows = 2 * static_cast<size_t>(sms) * kPreTile;
-  p->own_meta = reinterpret_cast<int2*>(take(static_cast<size_t>(n_seqs) * Hkv * row_tiles * 8));
+  p->own_meta = reinterpret_cast<int2*>(take(static_cast<size_t>(n_seqs) * Hkv * p->row_tiles * 8));
   p->own_slot_o = reinterpret_cast<float*>(take(own_rows * D * 4));
   p->own_slot_lse = reinterpret_cast<float*>(take(own_rows * 4));
   p->own_row_o = p->own_row_lse = p->pre_slot_o = p->pre_slot_lse = p->pre_row_o = p->pre_row_lse =
@@ -1106,8 +1218,10 @@ template <int D>
 oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   if (!once_per_device(attr_done, [] {
-        return cudaFuncSetAttribute(own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    OwnCfg<D>::kSmem) == cudaSuccess &&
+        return cudaFuncSetAttribute(own_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    OwnCfg<D, 1>::kSmem) == cudaSuccess &&
+               cudaFuncSetAttribute(own_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    OwnCfg<D, 2>::kSmem) == cudaSuccess &&
                cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     PreCfg<D>::kSmem) == cudaSuccess;
       }))
@@ -1131,10 +1245,15 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   if (!kv_map(&map, pool, std::min(p.P, kOwnTile), 2)) return OOMB_ERR_CUDA;
   if (e == cudaSuccess) {
     cfg.gridDim = dim3(own_ctas(sms, D));
-    cfg.blockDim = dim3(160);
-    cfg.dynamicSmemBytes = OwnCfg<D>::kSmem;
+    cfg.blockDim = dim3(kOwnThreads);
     cfg.numAttrs = p.n_groups > 0 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, own_kernel<D>, p, map);
+    if (p.own_rows == 8) {
+      cfg.dynamicSmemBytes = OwnCfg<D, 1>::kSmem;
+      e = cudaLaunchKernelEx(&cfg, own_kernel<D, 1>, p, map);
+    } else {
+      cfg.dynamicSmemBytes = OwnCfg<D, 2>::kSmem;
+      e = cudaLaunchKernelEx(&cfg, own_kernel<D, 2>, p, map);
+    }
   }
   if (e == cudaSuccess) {
     const int64_t rows = static_cast<int64_t>(p.n_seqs) * p.Hq;
@@ -1209,7 +1328,6 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   p.n_groups = a->n_groups;
   p.max_prefix_pages = a->max_prefix_pages;
   p.num_pages = d.num_pages;
-  p.row_tiles = (p.G + kOwnRows - 1) / kOwnRows;
   p.scale_log2 = a->softmax_scale * kLog2e;
   DeviceGuard guard(d.device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
