@@ -173,6 +173,17 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Barrier of own_kernel's warps 0-3.
+__device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // The transpose of an 8 x 8 matrix of 16-bit values spread over the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
@@ -190,14 +201,14 @@ template <int D, int NT>
 struct OwnCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kHalves = D / 64;
-  static constexpr int kStages = D == 128 ? 2 : 3;
-  static constexpr int kCtasPerSm = D == 128 ? 2 : 3;
+  static constexpr int kStages = 2;
+  static constexpr int kCtasPerSm = D == 64 ? 4 : NT == 1 ? 3 : 2;  // what shared memory holds
   static constexpr int kTileBytes = kOwnTile * D * 2 * 2;  // K and V
   static constexpr int kQRow = D * 2 + 16;                 // padded: ldmatrix without bank conflicts
   static constexpr int kQBytes = kRows * kQRow;
-  static constexpr int kORow = D + 4;
-  static constexpr int kOBytes = 4 * kRows * kORow * 4;
-  static constexpr int kSmem = kStages * (kTileBytes + kQBytes) + kOBytes + 1024;
+  static constexpr int kPRow = kOwnTile * 2 + 16;
+  static constexpr int kPBytes = kRows * kPRow;
+  static constexpr int kSmem = kStages * (kTileBytes + kQBytes) + 2 * kPBytes + 1024;
 };
 
 // What the producer tells the consumers of a tile.
@@ -213,10 +224,13 @@ struct TileInfo {
 // KV head no row of an instruction is empty, and half the exponentials, registers
 // and instructions go that 16 rows of queries would take; more heads are NT = 2
 // such columns on the same K and V fragments.
-// Warps 0-3 take 16 keys of each tile (of one page: pages have 16 tokens or
-// more) and keep a maximum, a sum and an O of their own, so they meet only at
-// the end of a unit; warp 4 fills the ring of tiles by TMA (K and V of a page
-// and head are neighbours in the pool: one box of both per 64 columns).
+// Warps 0-3 take 16 keys of each tile for the scores (of one page: pages have 16
+// tokens or more), exchange P through shared memory, and take a quarter of D each
+// for O += P V over all 64 keys: two barriers a tile, but O needs no joining at the
+// end of a unit, which short sequences would pay for most.  Warp 4 fills the ring of
+// tiles by TMA (K and V of a page and head are neighbours in the pool: one box of
+// both per 64 columns).  The number of barriers does not depend on what is found, so
+// a wait that gives up leaves nobody behind.
 constexpr int kOwnThreads = 160;
 template <int D, int NT>
 __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
@@ -227,14 +241,15 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sq = ring + Cfg::kStages * Cfg::kTileBytes;
-  float* so = reinterpret_cast<float*>(sq + Cfg::kStages * Cfg::kQBytes);
-  __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages], bar_put, bar_got;
+  uint8_t* sp = sq + Cfg::kStages * Cfg::kQBytes;
+  __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages];
   __shared__ TileInfo info[Cfg::kStages];
-  __shared__ float sm[4][kRows], sl[4][kRows];
+  // of a tile: maxima per warp and whether they move the running ones; of a unit: sums
+  __shared__ __align__(16) float sm[2][4][kRows], sl[2][4][kRows];
+  __shared__ __align__(16) int moved[2][4];
   __shared__ int abort_sh, issued_sh, used_sh;
   const int warp = warp_id(), lane = lane_id();
   volatile int* abort_flag = &abort_sh;
-
   pdl_launch_dependents();
   if (threadIdx.x == 128) prefetch_tensormap(&kvmap);
   if (threadIdx.x == 0) {
@@ -243,8 +258,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 4);
     }
-    mbar_init(&bar_put, 4);
-    mbar_init(&bar_got, 4);
     fence_mbar_init();
   }
   // heads past the unit's last stay zero: their scores would be NaN by chance
@@ -258,7 +271,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
     return static_cast<long long>(own_tiles(len)) * units_per_seq;
   });
   const int n_mine = static_cast<int>(rg.t1 - rg.t0);
-
 
   if (warp == 4) {
     // ------------------------------------------------------------ producer
@@ -372,23 +384,38 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
   } else {
     // ------------------------------------------------------------ consumers
     const int lg_r = min(__ffs(p.P) - 1, 6), R = 1 << lg_r, slots = kOwnTile >> lg_r;
-    // the 16 keys of this warp: slot and first row of it
-    const int my_slot = (warp * 16) >> lg_r, my_row = (warp * 16) & (R - 1);
     const uint32_t box_bytes = 2u * R * 128;
-    const uint32_t ring_at = smem_u32(ring), sq_at = smem_u32(sq);
-    // ldmatrix addresses: K (keys 0-15, two chunks of 8 columns), V transposed (two
-    // chunks of 8 columns, keys 0-7 and 8-15)
-    const int kr = my_row + (lane & 15), kc = lane >> 4;
-    const int vr = my_row + (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+    const uint32_t ring_at = smem_u32(ring), sq_at = smem_u32(sq), sp_at = smem_u32(sp);
+    constexpr int MT = D / 64;  // 16-row tiles of this warp's D / 4 rows of O^T
+    // ldmatrix addresses in a tile.  K: this warp's 16 keys (slot and row of a box), two
+    // chunks of 8 columns.  V transposed: two chunks of 8 of this warp's columns, keys
+    // 0-7 and 8-15 of each 16.
+    const int kr = ((warp * 16) & (R - 1)) + (lane & 15), kc = lane >> 4;
+    const uint32_t k_at = ((warp * 16) >> lg_r) * box_bytes + kr * 128;
+    const int col0 = warp * (D / 4);
+    const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (col0 % 64) / 8 + ((lane >> 3) & 1);
+    const uint32_t v_at = (col0 / 64) * slots * box_bytes + R * 128 + vr * 128;
+    // the scores' thread: keys lane / 4 and + 8, heads (lane % 4) 2 + {0, 1}
+    const int hd = (lane & 3) * 2;
     uint32_t qf[NT][D / 16][2];
-    float acc[NT][D / 16][4], m[NT][2], l[NT][2];
+    float acc[NT][MT][4], m[NT][2], l[NT][2];
     int used = 0, n_units = 0;
     bool ok = true;
     for (int i = 0; i < n_mine; ++i) {
-      const int st = i % Cfg::kStages;
-      if (!(ok = warp_wait(&full[st], (i / Cfg::kStages) & 1, abort_flag))) break;
-      ++used;
-      const TileInfo t = info[st];
+      const int st = i % Cfg::kStages, buf = i & 1;
+      if (ok) {
+        ok = warp_wait(&full[st], (i / Cfg::kStages) & 1, abort_flag);
+        if (!ok) {
+          *abort_flag = 1;
+          if (lane == 0) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+        }
+      }
+      TileInfo t{};
+      if (ok) {
+        t = info[st];
+        ++used;
+      }
+      const uint32_t tile_at = ring_at + st * Cfg::kTileBytes;
       if (t.flags & 1) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -398,7 +425,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
                       (lane >> 3) * 16,
                   qf[n][kk]);
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c)
+          for (int c = 0; c < MT; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[n][c][e] = 0.f;
           m[n][0] = m[n][1] = -INFINITY;
@@ -406,10 +433,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
         }
       }
       const int lim = t.lim - warp * 16;  // valid keys of this warp
-      if (lim > 0 && !((t.bad >> warp) & 1)) {
-        const uint32_t base = ring_at + st * Cfg::kTileBytes + my_slot * box_bytes;
-        // thread: keys lane / 4 and + 8, heads (lane % 4) 2 + {0, 1}; two chains of products
-        float s[NT][4], s2[NT][4];
+      const bool here = lim > 0 && !((t.bad >> warp) & 1);
+      float s[NT][4];
+      bool need = false;
+      if (here) {
+        float s2[NT][4];  // two chains of products
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -417,55 +445,67 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           uint32_t kb[4];
-          ldsm4(base + (kk / 4) * slots * box_bytes + kr * 128 +
-                    ((((kk % 4) * 2 + kc) ^ (kr & 7)) << 4),
+          ldsm4(tile_at + k_at + (kk / 4) * slots * box_bytes + ((((kk % 4) * 2 + kc) ^ (kr & 7)) << 4),
                 kb);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             mma16816(kk & 1 ? s2[n] : s[n], kb, qf[n][kk][0], qf[n][kk][1]);
         }
-        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
-        const bool ragged = lim < 16;
-        if (ragged) {
-          // values behind the end count 0 times, but 0 times NaN is NaN
-          const int k0 = (lane & 3) * 2;
-          vm0 = (k0 < lim ? 0xffffu : 0u) | (k0 + 1 < lim ? 0xffff0000u : 0u);
-          vm1 = (k0 + 8 < lim ? 0xffffu : 0u) | (k0 + 9 < lim ? 0xffff0000u : 0u);
-        }
-        bool need = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s[n][e] = (s[n][e] + s2[n][e]) * p.scale_log2;
-            if (ragged && lane / 4 + (e >> 1) * 8 >= lim) s[n][e] = -INFINITY;
+            if (lim < 16 && lane / 4 + (e >> 1) * 8 >= lim) s[n][e] = -INFINITY;
           }
           need |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kRescaleThreshold ||
                   fmaxf(s[n][1], s[n][3]) > m[n][1] + kRescaleThreshold;
         }
-        // the maximum over the keys is only taken when one of them is too far above it
-        if (__any_sync(0xffffffffu, need)) {
+        need = __any_sync(0xffffffffu, need);
+        if (need) {  // the maximum is only taken when a key is too far above the running one
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float mt = fmaxf(s[n][e], s[n][e + 2]);
               mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
               mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
               mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-              if (mt <= m[n][e]) continue;
-              const float a = fast_exp2(m[n][e] - mt);
-              m[n][e] = mt;
-              l[n][e] *= a;
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                acc[n][c][e] *= a;
-                acc[n][c][e + 2] *= a;
-              }
+              if (lane < 4) sm[buf][warp][n * 8 + hd + e] = mt;
             }
+        }
+      }
+      if (lane == 0) moved[buf][warp] = need;
+      consumer_barrier();
+      const int4 mv = *reinterpret_cast<const int4*>(moved[buf]);
+      if (mv.x | mv.y | mv.z | mv.w) {
+        const int by[4] = {mv.x, mv.y, mv.z, mv.w};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float2 top = make_float2(m[n][0], m[n][1]);
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (by[w]) {
+              const float2 x = *reinterpret_cast<const float2*>(&sm[buf][w][n * 8 + hd]);
+              top = make_float2(fmaxf(top.x, x.x), fmaxf(top.y, x.y));
+            }
+          const float a0 = top.x > m[n][0] ? fast_exp2(m[n][0] - top.x) : 1.f;
+          const float a1 = top.y > m[n][1] ? fast_exp2(m[n][1] - top.y) : 1.f;
+          m[n][0] = top.x;
+          m[n][1] = top.y;
+          l[n][0] *= a0;
+          l[n][1] *= a1;
+#pragma unroll
+          for (int c = 0; c < MT; ++c) {
+            acc[n][c][0] *= a0;
+            acc[n][c][1] *= a1;
+            acc[n][c][2] *= a0;
+            acc[n][c][3] *= a1;
           }
         }
-        uint32_t pb[NT][2];
+      }
+      const uint32_t p_at = sp_at + buf * Cfg::kPBytes;
+      if (here) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
@@ -474,22 +514,50 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
           const float p2 = fast_exp2(s[n][2] - m0), p3 = fast_exp2(s[n][3] - m1);
           l[n][0] += p0 + p2;
           l[n][1] += p1 + p3;
-          pb[n][0] = transpose8(pack_bf16(p0, p1));
-          pb[n][1] = transpose8(pack_bf16(p2, p3));
+          // P [head][key]: head lane / 4, keys (lane % 4) 2 + {0, 1} and + 8
+          const uint32_t at = p_at + (n * 8 + lane / 4) * Cfg::kPRow + warp * 32 + hd * 2;
+          sts32(at, transpose8(pack_bf16(p0, p1)));
+          sts32(at + 16, transpose8(pack_bf16(p2, p3)));
         }
-        const uint32_t vbase = base + R * 128 + vr * 128;
+      }
+      if (t.flags & 2) {  // the unit's sums over this warp's keys
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+            if (lane < 4) sl[n_units & 1][warp][n * 8 + hd + e] = l[n][e];
+          }
+      }
+      consumer_barrier();
+      if (!ok) continue;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {  // keys [16 ks, 16 ks + 16)
+        const int left = t.lim - 16 * ks;
+        if (left <= 0) break;
+        if ((t.bad >> ks) & 1) continue;
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          ldsm2(p_at + (n * 8 + (lane & 7)) * Cfg::kPRow + ks * 32 + ((lane >> 3) & 1) * 16, pf[n]);
+        const uint32_t at = tile_at + v_at + ((16 * ks) >> lg_r) * box_bytes + ((16 * ks) & (R - 1)) * 128;
+#pragma unroll
+        for (int c = 0; c < MT; ++c) {
           uint32_t va[4];
-          ldsm4t(vbase + (c / 4) * slots * box_bytes + ((((c % 4) * 2 + vc) ^ (vr & 7)) << 4), va);
-          if (ragged) {
-            va[0] &= vm0;
-            va[1] &= vm0;
-            va[2] &= vm1;
-            va[3] &= vm1;
+          ldsm4t(at + (((vc + 2 * c) ^ (vr & 7)) << 4), va);
+          if (left < 16) {
+            // values behind the end count 0 times, but 0 times NaN is NaN
+            const uint32_t lo = (hd < left ? 0xffffu : 0u) | (hd + 1 < left ? 0xffff0000u : 0u);
+            const uint32_t hi = (hd + 8 < left ? 0xffffu : 0u) | (hd + 9 < left ? 0xffff0000u : 0u);
+            va[0] &= lo;
+            va[1] &= lo;
+            va[2] &= hi;
+            va[3] &= hi;
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(acc[n][c], va, pb[n][0], pb[n][1]);
+          for (int n = 0; n < NT; ++n) mma16816(acc[n][c], va, pf[n][0], pf[n][1]);
         }
       }
       __syncwarp();
@@ -497,94 +565,58 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
       if (!(t.flags & 2)) continue;
 
       // ---------------------------------------------------------- end of a unit
-      const int b = t.b, h0 = t.h0, rows = t.rows;
-      // the last unit's sums have been read by all
-      if (n_units > 0 && !(ok = warp_wait(&bar_got, (n_units - 1) & 1, abort_flag))) break;
+      const bool whole = t.flags & 4, direct = whole && p.n_groups == 0;
+      const size_t row0 = static_cast<size_t>(t.b) * p.Hq + t.h0;
+      const size_t slot0 = (static_cast<size_t>(blockIdx.x) * 2 + (t.flags & 8 ? 1 : 0)) * kRows;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        float2 total = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-          const int row = n * 8 + (lane & 3) * 2 + e;
-          if (lane < 4) {
-            sm[warp][row] = m[n][e];
-            sl[warp][row] = l[n][e];
-          }
-          // O^T of head `row`: 16 c + lane / 4 and + 8
-          if (m[n][e] == -INFINITY) continue;  // no keys here: not read
-          float* dst = so + (warp * kRows + row) * Cfg::kORow + lane / 4;
+        for (int w = 0; w < 4; ++w) {
+          const float2 x = *reinterpret_cast<const float2*>(&sl[n_units & 1][w][n * 8 + hd]);
+          total = make_float2(total.x + x.x, total.y + x.y);
+        }
+        const float i0 = total.x > 0.f ? __fdividef(1.f, total.x) : 0.f;
+        const float i1 = total.y > 0.f ? __fdividef(1.f, total.y) : 0.f;
+        if (warp == 0 && lane < 4) {
+          const float lse[2] = {total.x > 0.f ? m[n][0] + __log2f(total.x) : -INFINITY,
+                                total.y > 0.f ? m[n][1] + __log2f(total.y) : -INFINITY};
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            dst[16 * c] = acc[n][c][e];
-            dst[16 * c + 8] = acc[n][c][e + 2];
+          for (int e = 0; e < 2; ++e) {
+            const int row = n * 8 + hd + e;
+            if (row >= t.rows) continue;
+            if (!direct) (whole ? p.own_row_lse + row0 : p.own_slot_lse + slot0)[row] = lse[e];
+            else if (p.lse) p.lse[row0 + row] = kLn2 * lse[e];
           }
         }
+        if (direct) {
+          const int row = n * 8 + lane / 4;
+          __nv_bfloat16* dst = p.o + t.b * p.o_stride + (t.h0 + row) * D + col0 + hd;
+#pragma unroll
+          for (int c = 0; c < MT; ++c) {
+            const uint32_t x = transpose8(pack_bf16(acc[n][c][0] * i0, acc[n][c][1] * i1));
+            const uint32_t y = transpose8(pack_bf16(acc[n][c][2] * i0, acc[n][c][3] * i1));
+            if (row < t.rows) {
+              *reinterpret_cast<uint32_t*>(dst + 16 * c) = x;
+              *reinterpret_cast<uint32_t*>(dst + 16 * c + 8) = y;
+            }
+          }
+        } else {
+          float* dst = (whole ? p.own_row_o + row0 * D : p.own_slot_o + slot0 * D) +
+                       (n * 8 + hd) * D + col0 + lane / 4;
+#pragma unroll
+          for (int c = 0; c < MT; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (n * 8 + hd + e < t.rows) {
+                dst[e * D + 16 * c] = acc[n][c][e] * (e ? i1 : i0);
+                dst[e * D + 16 * c + 8] = acc[n][c][e + 2] * (e ? i1 : i0);
+              }
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_put);
-      if (!(ok = warp_wait(&bar_put, n_units & 1, abort_flag))) break;
       ++n_units;
-      constexpr int TPR = D / 4, RPW = 32 / TPR;  // lanes of a row, rows of a warp
-      const bool whole = t.flags & 4;
-      const bool begins_before = !(t.flags & 8);
-      const int d4 = (lane % TPR) * 4;
-      // two rows at a time, so that their chains overlap
-      for (int row0 = warp * RPW + lane / TPR; row0 < rows; row0 += 8 * RPW) {
-        float top[2], total[2], mw[2][4];
-        float4 x[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = min(row0 + k * 4 * RPW, kRows - 1);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) mw[k][w] = sm[w][row];
-          top[k] = fmaxf(fmaxf(mw[k][0], mw[k][1]), fmaxf(mw[k][2], mw[k][3]));
-          total[k] = 0.f;
-          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            if (mw[k][w] == -INFINITY) continue;  // a warp that had no keys
-            const float f = fast_exp2(mw[k][w] - top[k]);
-            const float4 y =
-                *reinterpret_cast<const float4*>(so + (w * kRows + row) * Cfg::kORow + d4);
-            total[k] = fmaf(f, sl[w][row], total[k]);
-            x[k].x = fmaf(f, y.x, x[k].x);
-            x[k].y = fmaf(f, y.y, x[k].y);
-            x[k].z = fmaf(f, y.z, x[k].z);
-            x[k].w = fmaf(f, y.w, x[k].w);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = row0 + k * 4 * RPW;
-          if (row >= rows) break;
-          const float inv = total[k] > 0.f ? 1.f / total[k] : 0.f;
-          const float lse2 = total[k] > 0.f ? top[k] + log2f(total[k]) : -INFINITY;
-          const float4 y = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
-          const size_t out_row = static_cast<size_t>(b) * p.Hq + h0 + row;
-          if (whole && p.n_groups == 0) {
-            *reinterpret_cast<uint2*>(p.o + b * p.o_stride + (h0 + row) * D + d4) =
-                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-            if (d4 == 0 && p.lse) p.lse[out_row] = kLn2 * lse2;
-          } else {
-            const size_t slot_row =
-                (static_cast<size_t>(blockIdx.x) * 2 + (begins_before ? 0 : 1)) * kRows + row;
-            float* od = whole ? p.own_row_o + out_row * D : p.own_slot_o + slot_row * D;
-            float* ld = whole ? p.own_row_lse + out_row : p.own_slot_lse + slot_row;
-            *reinterpret_cast<float4*>(od + d4) = y;
-            if (d4 == 0) *ld = lse2;
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_got);
     }
-    if (!ok) {
-      *abort_flag = 1;
-      if (lane == 0) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
-    }
-    if (warp == 0 && lane == 0) used_sh = used;
+    if (threadIdx.x == 0) used_sh = used;
   }
   __syncthreads();
   // after an abort, wait (bounded) for loads still landing in shared memory
@@ -1165,11 +1197,12 @@ bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_gr
          static_cast<int64_t>(n_seqs) * Hq <= INT32_MAX;
 }
 
-int own_ctas(int sms, int D) {
-  return sms * (D == 128 ? OwnCfg<128, 1>::kCtasPerSm : OwnCfg<64, 1>::kCtasPerSm);
-}
 // Query heads of a unit of own_kernel: one column of 8, or two.
 int own_unit_rows(int G) { return G <= 8 ? 8 : 16; }
+int own_ctas(int sms, int D, int rows) {
+  return sms * (D == 128 ? rows == 8 ? OwnCfg<128, 1>::kCtasPerSm : OwnCfg<128, 2>::kCtasPerSm
+                         : OwnCfg<64, 1>::kCtasPerSm);
+}
 
 // Lays the workspace out from `base` (null: only counts) and returns its bytes.
 size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, int sms,
@@ -1184,7 +1217,7 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   const int G = Hq / Hkv;
   p->own_rows = own_unit_rows(G);
   p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
-  const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D)) * p->own_rows;
+  const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D, p->own_rows)) * p->own_rows;
   const size_t pre_rows = 2 * static_cast<size_t>(sms) * kPreTile;
   p->own_meta = reinterpret_cast<int2*>(take(static_cast<size_t>(n_seqs) * Hkv * p->row_tiles * 8));
   p->own_slot_o = reinterpret_cast<float*>(take(own_rows * D * 4));
@@ -1244,7 +1277,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   }
   if (!kv_map(&map, pool, std::min(p.P, kOwnTile), 2)) return OOMB_ERR_CUDA;
   if (e == cudaSuccess) {
-    cfg.gridDim = dim3(own_ctas(sms, D));
+    cfg.gridDim = dim3(own_ctas(sms, D, p.own_rows));
     cfg.blockDim = dim3(kOwnThreads);
     cfg.numAttrs = p.n_groups > 0 ? 1 : 0;
     if (p.own_rows == 8) {
