@@ -7,8 +7,8 @@
 //   LSE = ln sum e^LSE_k,  O = sum e^(LSE_k - LSE) O_k.
 //
 // Three kernels, each a dependent launch of the one before:
-//   prefix_kernel (with prefix groups)  128 rows (sequence, head) of a group at
-//       once against the prefix's keys: its K and V are read once per 128 rows
+//   prefix_kernel (with prefix groups)  256 rows (sequence, head) of a group at
+//       once against the prefix's keys: its K and V are read once per 256 rows
 //       instead of once per sequence.  tcgen05, bound by the tensor cores and
 //       the exponentials for many rows, by memory for few.
 //   own_kernel   8 or 16 query heads of one KV head of one sequence against its
@@ -63,11 +63,13 @@ struct DecodeParams {
   float* own_slot_lse;
   float* own_row_o;
   float* own_row_lse;
-  int2* pre_meta;  // [n_seqs Hq]
+  // of a prefix: [n_seqs Hq] {first CTA, 2 CTAs + whether the unit was split}; a slot
+  // per softmax lane; the second rows are lane 1's of a whole split unit
+  int2* pre_meta;
   float* pre_slot_o;
   float* pre_slot_lse;
-  float* pre_row_o;
-  float* pre_row_lse;
+  float* pre_row_o[2];
+  float* pre_row_lse[2];
 };
 
 __device__ __forceinline__ void pdl_launch_dependents() {
@@ -632,19 +634,20 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
 template <int D>
 struct PreCfg {
   static constexpr int kHalves = D / 64;
-  static constexpr int kTileBytes = kPreTile * D * 2;  // K or V tile
-  static constexpr int kNK = 3;
-  static constexpr int kNV = 3;
-  static constexpr int kSmem = kTileBytes * (kNK + kNV) + 1024;
+  static constexpr int kTileBytes = kPreTile * D * 2;  // Q, K or V tile
+  static constexpr int kSlots = D == 128 ? 5 : 10;     // of the ring that K and V tiles share
+  static constexpr int kSmem = kTileBytes * (2 + kSlots) + 1024;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kColO = 256;
-  static constexpr uint32_t kColQ = 384;
 };
+constexpr int kPreThreads = 384;
 
-// Steps through the CTA's tiles: of unit u = (KV head, row tile) of group j.
+// Steps through the CTA's share.  A unit is one KV head and up to 256 rows of a
+// group, 128 for each of the two softmax lanes; both take the same key tile in a
+// step.  Where only 128 rows are left, both lanes have these rows and take two key
+// tiles a step (`split`), lane 1 every second one.
 struct PreWalk {
   Group gr;
-  int j, u, tile;
+  int j, g, pair, step;
   int nt, row_tiles;
   __device__ __forceinline__ void load(const DecodeParams& p, uint32_t* status = nullptr) {
     gr = group_of(p, j, status);
@@ -652,21 +655,35 @@ struct PreWalk {
     row_tiles = static_cast<int>(
         (static_cast<long long>(gr.hi - gr.lo) * p.G + kPreTile - 1) / kPreTile);
   }
-  __device__ __forceinline__ long long weight(const DecodeParams& p) const {
-    return static_cast<long long>(nt) * row_tiles * p.Hkv;
+  // steps of one KV head, and of the group
+  __device__ __forceinline__ long long head_steps() const {
+    return static_cast<long long>(row_tiles / 2) * nt + (row_tiles & 1) * ((nt + 1) / 2);
   }
+  __device__ __forceinline__ long long weight(const DecodeParams& p) const {
+    return head_steps() * p.Hkv;
+  }
+  __device__ __forceinline__ bool split() const { return 2 * pair + 1 == row_tiles; }
+  __device__ __forceinline__ int steps() const { return split() ? (nt + 1) / 2 : nt; }
+  // key tile of a lane in this step; it has none where this is not below nt
+  __device__ __forceinline__ int tile(int ln) const { return split() ? 2 * step + ln : step; }
   __device__ __forceinline__ void start(const DecodeParams& p, const Range& r) {
     j = r.item;
     load(p);
-    const long long off = r.t0 - r.item_at;
-    u = static_cast<int>(fast_div(off, nt));
-    tile = static_cast<int>(off - static_cast<long long>(u) * nt);
+    const long long off = r.t0 - r.item_at, hs = head_steps();
+    g = static_cast<int>(fast_div(off, hs));
+    const long long rem = off - g * hs;
+    pair = static_cast<int>(min(fast_div(rem, nt), static_cast<long long>(row_tiles / 2)));
+    step = static_cast<int>(rem - static_cast<long long>(pair) * nt);
   }
-  __device__ __forceinline__ void next(const DecodeParams& p, bool more) {
-    if (++tile < nt) return;
-    tile = 0;
-    if (++u < row_tiles * p.Hkv) return;
-    u = 0;
+  // n steps on, within the unit or to the start of the next one
+  __device__ __forceinline__ void skip(const DecodeParams& p, int n, bool more) {
+    step += n;
+    if (step < steps()) return;
+    step = 0;
+    if (++pair < (row_tiles + 1) / 2) return;
+    pair = 0;
+    if (++g < p.Hkv) return;
+    g = 0;
     if (!more) return;
     do {
       ++j;
@@ -675,59 +692,73 @@ struct PreWalk {
   }
 };
 
-// 128 rows (sequence, query head of the KV head) of a group against 128 keys a
-// tile.  Warps 0-3: thread r owns row r (TMEM lane r): its query goes to TMEM
-// once per unit, its scores come back from TMEM, p = 2^x goes to TMEM in their
-// place, O is rescaled when the maximum moves, and normalised at the end.  Warp 4
-// loads K tiles by TMA, warp 6 V tiles, warp 5 issues the products (S = Q K^T into
-// one of two buffers, O += P V).
-// TMEM columns: S0 [0,128), S1 [128,256), O [256,256+D), Q [384,384+D/2).
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 256 rows (sequence, query head of the KV head) of a group against 128 keys a
+// step.  Warps 0-3 and 4-7 are two softmax lanes of 128 rows each (thread r owns
+// row r, TMEM lane r): scores come from TMEM, p = 2^x goes back in their place, O
+// is rescaled when the maximum moves, and normalised at the end.  While one lane
+// computes, the tensor core does the other's O += P V and next S = Q K^T: one lane
+// alone would leave it idle for the softmax's latency.  Warp 8 loads K and V tiles by
+// TMA, warp 9 issues the products, in the order
+//   S0 S1 | PV0 S0' PV1 S1' | PV0' S0'' PV1' S1'' ...
+// so a lane's scores are complete only after its last O += P V: O stands still while
+// the lane looks at them.  TMEM columns: S of lane 0 and 1 [0,128) [128,256) (P in
+// their first half), O [256,384) [384,512).  Q is in shared memory, written by its
+// lane's threads.
 template <int D>
-__global__ void __launch_bounds__(224, 1)
+__global__ void __launch_bounds__(kPreThreads, 1)
     prefix_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kvmap) {
   using Cfg = PreCfg<D>;
+  constexpr int NS = Cfg::kSlots;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sK = reinterpret_cast<uint8_t*>(
+  uint8_t* sQ = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sV = sK + Cfg::kNK * Cfg::kTileBytes;
-  __shared__ uint64_t bar_qt, bar_drain, bar_o, bar_fin;
-  __shared__ uint64_t bar_kf[Cfg::kNK], bar_ke[Cfg::kNK], bar_vf[Cfg::kNV], bar_ve[Cfg::kNV];
-  __shared__ uint64_t bar_s[2], bar_p[2];
+  uint8_t* ring = sQ + 2 * Cfg::kTileBytes;
+  __shared__ uint64_t full[NS], empty[NS];
+  __shared__ uint64_t bar_q[2], bar_s[2], bar_p[2], bar_fin[2], bar_drain;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-  __shared__ int k_issued_sh, v_issued_sh, k_used_sh, v_used_sh;
+  __shared__ int abort_sh, issued_sh;
   const int warp = warp_id(), lane = lane_id();
   pdl_launch_dependents();
+  if (threadIdx.x == 256) prefetch_tensormap(&kvmap);
   if (threadIdx.x == 0) {
-    abort_sh = 0;
-    k_issued_sh = v_issued_sh = k_used_sh = v_used_sh = 0;
-    mbar_init(&bar_qt, 4);
-    mbar_init(&bar_drain, 1);
-    mbar_init(&bar_o, 1);
-    mbar_init(&bar_fin, 1);
-    for (int i = 0; i < Cfg::kNK; ++i) {
-      mbar_init(&bar_kf[i], 1);
-      mbar_init(&bar_ke[i], 1);
-    }
-    for (int i = 0; i < Cfg::kNV; ++i) {
-      mbar_init(&bar_vf[i], 1);
-      mbar_init(&bar_ve[i], 1);
+    abort_sh = issued_sh = 0;
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_q[i], 4);
       mbar_init(&bar_s[i], 1);
       mbar_init(&bar_p[i], 4);
+      mbar_init(&bar_fin[i], 1);
     }
+    mbar_init(&bar_drain, 1);
     fence_mbar_init();
   }
-  const Range rg = find_range<224>(p.n_groups, [&](int j, bool note) {
+  const Range rg = find_range<kPreThreads>(p.n_groups, [&](int j, bool note) {
     PreWalk w;
     w.j = j;
     w.load(p, note && blockIdx.x == 0 ? p.status : nullptr);
     return w.weight(p);
   });
   if (rg.t0 >= rg.t1) return;  // the same for all threads of the CTA
-  const int n_mine = static_cast<int>(rg.t1 - rg.t0);
-  if (warp == 0) {
+  const int n_mine = static_cast<int>(rg.t1 - rg.t0), per = static_cast<int>(rg.per);
+  if (warp == 8) {
     tmem_alloc(&tmem_base_sh, Cfg::kTmemCols);
     tmem_relinquish();
   }
@@ -736,281 +767,318 @@ __global__ void __launch_bounds__(224, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   volatile int* abort_flag = &abort_sh;
-  PreWalk w;
-  w.start(p, rg);
-  const int per = kPreTile / p.P;  // pages of a tile
 
-  if (warp == 4 || warp == 6) {
-    // ------------------------------------------------------------ producers
-    if (lane == 0) {
-      const bool is_k = warp == 4;
-      prefetch_tensormap(&kvmap);
-      const int nst = is_k ? Cfg::kNK : Cfg::kNV;
-      uint64_t* full = is_k ? bar_kf : bar_vf;
-      uint64_t* empty = is_k ? bar_ke : bar_ve;
-      uint8_t* base = is_k ? sK : sV;
-      int issued = 0;
-      for (int i = 0; i < n_mine; ++i) {
-        const int32_t* table = p.prefix_pages + static_cast<size_t>(w.j) * p.max_prefix_pages;
-        int pg[8];
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const int li = w.tile * per + s;
-          // a page past the prefix, or one that is none: beyond the pool, filled with zeros
-          pg[s] = p.num_pages;
-          if (s < per && static_cast<long long>(li) * p.P < w.gr.len) {
-            const int id = table[li];
-            if (id >= 0 && id < p.num_pages) pg[s] = id;
-            else if (is_k) atomicOr(p.status, OOMB_DEV_BAD_PAGE);
+  if (warp >= 8) {
+    reg_dec<56>();
+    if (warp == 8) {
+      // ---------------------------------------------------------- loads
+      PreWalk w;
+      w.start(p, rg);
+      const int lg_p = __ffs(p.P) - 1, per_tile = kPreTile >> lg_p;
+      const int s = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;  // this lane's box
+      int ids = 0, ids_j = -1, first_id = 0, issued = 0;
+      bool ok = true;
+      // tile `t` of the current group: K (which 0) or V (1)
+      auto load = [&](int t, int which) {
+        const int pg0 = t * per_tile;
+        if (ids_j != w.j || pg0 < first_id || pg0 + per_tile > first_id + 32) {
+          ids_j = w.j;
+          first_id = pg0;
+          const int at = pg0 + lane;
+          ids = p.num_pages;  // beyond the pool: filled with zeros
+          if (static_cast<long long>(at) * p.P < w.gr.len) {
+            ids = p.prefix_pages[static_cast<size_t>(w.j) * p.max_prefix_pages + at];
+            if (ids < 0 || ids >= p.num_pages) {
+              atomicOr(p.status, OOMB_DEV_BAD_PAGE);
+              ids = p.num_pages;
+            }
           }
         }
-        const int g = w.u / w.row_tiles, st = i % nst;
-        if (!mbar_wait(&empty[st], ((i / nst) & 1) ^ 1, abort_flag)) break;
-        mbar_arrive_expect_tx(&full[st], Cfg::kTileBytes);
-        uint8_t* dst = base + st * Cfg::kTileBytes;
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-          if (s < per)
-            for (int hf = 0; hf < Cfg::kHalves; ++hf)
-              tma_load_4d(dst + hf * kPreTile * 128 + s * p.P * 128, &kvmap, &full[st], hf * 64, 0,
-                          2 * g + (is_k ? 0 : 1), pg[s]);
+        const int page = __shfl_sync(0xffffffffu, ids, (pg0 - first_id + s) & 31);
+        const int st = issued % NS;
+        int good = 1;
+        if (lane == 0) {
+          good = mbar_wait(&empty[st], ((issued / NS) & 1) ^ 1, abort_flag);
+          if (good) mbar_arrive_expect_tx(&full[st], Cfg::kTileBytes);
+        }
+        if (!__shfl_sync(0xffffffffu, good, 0)) return false;
         ++issued;
-        w.next(p, i + 1 < n_mine);
-      }
-      if (*abort_flag) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
-      if (is_k) k_issued_sh = issued;
-      else v_issued_sh = issued;
-    }
-  } else if (warp == 5) {
-    // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
-      const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV);
-      int k_used = 0, v_used = 0, n_units = 0;
-      bool ok = true, first = false, last = false;
-      // O += P V of tile i; `fst`: the first of its unit, `lst`: the last
-      auto pv = [&](int i, bool fst, bool lst) {
-        const int b = i & 1, vs = i % Cfg::kNV;
-        if (!mbar_wait(&bar_p[b], (i >> 1) & 1, abort_flag)) return false;
-        if (!mbar_wait(&bar_vf[vs], (i / Cfg::kNV) & 1, abort_flag)) return false;
-        ++v_used;
-        tc_fence_after();
-        const uint32_t vb = v_addr + vs * Cfg::kTileBytes;
-#pragma unroll
-        for (int kk = 0; kk < kPreTile / 16; ++kk)
-          umma_ts(tmem + Cfg::kColO, tmem + b * 128 + kk * 8,
-                  sw128_desc(vb + kk * 16 * 128, kPreTile * 128, 1024), idesc_pv,
-                  (!fst || kk > 0) ? 1u : 0u);
-        umma_commit(&bar_ve[vs]);
-        umma_commit(&bar_o);
-        if (lst) umma_commit(&bar_fin);
+        if (s < per_tile)
+          tma_load_4d(ring + st * Cfg::kTileBytes + hf * kPreTile * 128 + ((s << lg_p) * 128), &kvmap,
+                      &full[st], hf * 64, 0, 2 * w.g + which, page);
         return true;
       };
-      for (int i = 0; ok && i <= n_mine; ++i) {
-        const bool was_first = first, was_last = last;
-        bool done = i == 0;
-        if (i < n_mine) {
-          first = i == 0 || w.tile == 0;
-          last = i == n_mine - 1 || w.tile == w.nt - 1;
-          if (first) {
-            // the new unit's queries come when the old one's O has been read
-            if (!done && !(ok = pv(i - 1, was_first, was_last))) break;
-            done = true;
-            if (!(ok = mbar_wait(&bar_qt, n_units & 1, abort_flag))) break;
-            ++n_units;
-          }
-          const int ks = i % Cfg::kNK;
-          if (!(ok = mbar_wait(&bar_kf[ks], (i / Cfg::kNK) & 1, abort_flag))) break;
-          ++k_used;
-          tc_fence_after();
-          const uint32_t sd = tmem + (i & 1) * 128;
-          const uint32_t kb = k_addr + ks * Cfg::kTileBytes;
+      for (int i = 0; ok && i < n_mine; ++i) {
+        const int ta = w.tile(0), tb = w.tile(1);
+        const bool two = w.split() && tb < w.nt;
+        ok = load(ta, 0) && (!two || load(tb, 0)) && load(ta, 1) && (!two || load(tb, 1));
+        w.skip(p, 1, i + 1 < n_mine);
+      }
+      if (lane == 0) {
+        issued_sh = issued;
+        if (*abort_flag) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- products
+      // The whole warp goes through this code with the same values in every lane (those
+      // that come from memory are made so by a shuffle): the descriptors then live in
+      // uniform registers.  Issued from a branch of one lane, each product first moves
+      // its operands there, and takes twice the tensor core's time.
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+      // low words of the descriptors (address / 16, leading offset); the high words are constant
+      constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+      constexpr uint32_t kTile16 = Cfg::kTileBytes >> 4;
+      const uint32_t q_lo = (smem_u32(sQ) >> 4) | (1u << 16);
+      const uint32_t k_lo = (smem_u32(ring) >> 4) | (1u << 16);
+      const uint32_t v_lo = (smem_u32(ring) >> 4) | (((kPreTile * 128u) >> 4) << 16);
+      PreWalk w;
+      w.start(p, rg);
+      int n_s[2] = {0, 0}, n_units[2] = {0, 0};  // S products and units of a lane so far
+      int cnt = 0;                               // tiles of the ring before this step
+      bool ok = true;
+      auto wait_tile = [&](int c) { return warp_wait(&full[c % NS], (c / NS) & 1, abort_flag); };
+      auto qk = [&](int ln, int c, bool release) {  // S = Q K^T
+        if (!wait_tile(c)) return false;
+        tc_fence_after();
+        const uint32_t a = q_lo + ln * kTile16, b = k_lo + (c % NS) * kTile16;
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (kPreTile * 128) + (kk % 4) * 32;
-            umma_ts(sd, tmem + Cfg::kColQ + kk * 8, sw128_desc(kb + off, 16, 1024), idesc_s,
-                    kk > 0);
+            const uint32_t off = ((kk / 4) * (kPreTile * 128) + (kk % 4) * 32) >> 4;
+            umma_ss(tmem + ln * 128, desc64(a + off, kHi), desc64(b + off, kHi), idesc_s, kk > 0);
           }
-          umma_commit(&bar_ke[ks]);
-          umma_commit(&bar_s[i & 1]);
-          w.next(p, i + 1 < n_mine);
+          if (release) umma_commit(&empty[c % NS]);
+          umma_commit(&bar_s[ln]);
         }
-        if (!done) ok = pv(i - 1, was_first, was_last);
+        __syncwarp();
+        ++n_s[ln];
+        return true;
+      };
+      auto pv = [&](int ln, int c, bool fresh, bool release, bool last) {  // O += P V
+        if (!warp_wait(&bar_p[ln], (n_s[ln] - 1) & 1, abort_flag) || !wait_tile(c)) return false;
+        tc_fence_after();
+        const uint32_t b = v_lo + (c % NS) * kTile16;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kPreTile / 16; ++kk)
+            umma_ts(tmem + 256 + ln * 128, tmem + ln * 128 + kk * 8, desc64(b + kk * 128, kHi),
+                    idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+          if (release) umma_commit(&empty[c % NS]);
+          if (last) umma_commit(&bar_fin[ln]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int left = n_mine; ok && left > 0;) {
+        // a unit: its steps here, whether lane 1 has a tile of its own, and in the last step
+        const int here = __shfl_sync(0xffffffffu, min(left, w.steps() - w.step), 0);
+        const bool split = __shfl_sync(0xffffffffu, w.split(), 0);
+        const bool odd = __shfl_sync(
+            0xffffffffu, w.split() && w.step + here == w.steps() && (w.nt & 1), 0);
+        left -= here;
+        // the lanes' queries come when the old unit's O has been read
+        const bool two0 = !(odd && here == 1);
+        for (int ln = 0; ok && ln < 1 + two0; ++ln)
+          ok = warp_wait(&bar_q[ln], n_units[ln]++ & 1, abort_flag);
+        ok = ok && qk(0, cnt, split || !two0);
+        ok = ok && (!two0 || qk(1, cnt + split, true));
+        for (int i = 0; ok && i < here; ++i) {
+          const bool more = i + 1 < here;
+          const bool two = more || !odd, ntwo = more && (i + 2 < here || !odd);
+          const bool extra = split && two, nextra = split && ntwo;
+          const int va = cnt + 1 + extra, vb = va + extra;
+          cnt += 2 + 2 * extra;
+          ok = pv(0, va, i == 0, extra || !two, !more);
+          ok = ok && (!more || qk(0, cnt, nextra || !ntwo));
+          ok = ok && (!two || pv(1, vb, i == 0, true, !ntwo));
+          ok = ok && (!ntwo || qk(1, cnt + nextra, true));
+        }
+        w.skip(p, here, left > 0);
       }
       if (!ok) {
         *abort_flag = 1;
-        atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+        if (lane == 0) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
       }
       // every product of this CTA has completed once bar_drain fires
-      umma_commit(&bar_drain);
+      if (elect_one()) umma_commit(&bar_drain);
       mbar_wait_drain(&bar_drain, 0);
-      k_used_sh = k_used;
-      v_used_sh = v_used;
     }
   } else {
+    reg_inc<224>();
     // ------------------------------------------------------------ softmax
-    const int r = threadIdx.x;  // 0..127
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const int ln = warp / 4, r = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_off + ln * 128, to = tmem + lane_off + 256 + ln * 128;
+    const int lg_p = __ffs(p.P) - 1, per_tile = kPreTile >> lg_p;
+    PreWalk w;
+    w.start(p, rg);
     float m_used = -INFINITY, l = 0.f;
     size_t out_row = 0;
-    int n_units = 0;
-    bool ok = true, valid = false, begins = false;
+    int cnt = 0, n_s = 0, n_units = 0;
+    bool ok = true, valid = false, begins = false, any = false;
     for (int i = 0; ok && i < n_mine; ++i) {
-      const int b = i & 1;
-      const bool first = i == 0 || w.tile == 0;
-      if (first) {
-        // this thread's row of the unit; its query into TMEM (A operand of S = Q K^T)
-        const int g = w.u / w.row_tiles, rt = w.u % w.row_tiles;
-        const long long rr = static_cast<long long>(rt) * kPreTile + r;
-        const int seq = w.gr.lo + static_cast<int>(rr / p.G), h = g * p.G + static_cast<int>(rr % p.G);
+      const bool split = w.split();
+      const bool two = !split || w.tile(1) < w.nt, extra = split && two;
+      const int vc = cnt + 1 + extra + (extra ? ln : 0);  // ring index of this lane's V tile
+      cnt += 2 + 2 * extra;
+      const bool mine = ln == 0 || two;
+      if (i == 0 || w.step == 0) {
+        // this thread's row of the unit
+        const unsigned rr = (2u * w.pair + (split ? 0 : ln)) * kPreTile + r;
+        const unsigned rs = rr / static_cast<unsigned>(p.G);
+        const int seq = w.gr.lo + static_cast<int>(rs);
+        const int h = w.g * p.G + static_cast<int>(rr - rs * p.G);
         valid = seq < w.gr.hi;
-        begins = w.tile == 0;
+        begins = w.step == 0;
         out_row = static_cast<size_t>(seq) * p.Hq + h;
-        const __nv_bfloat16* qrow = p.q + seq * p.q_stride + h * D;
+        if (mine) {
+          // its query into shared memory (A operand, K-major, 128-byte swizzle)
+          const __nv_bfloat16* qrow = p.q + seq * p.q_stride + h * D;
+          uint4 v[D / 8];
 #pragma unroll
-        for (int hf = 0; hf < Cfg::kHalves; ++hf) {
-          uint32_t qv[32];
+          for (int ch = 0; ch < D / 8; ++ch)
+            v[ch] = valid ? *reinterpret_cast<const uint4*>(qrow + ch * 8) : make_uint4(0, 0, 0, 0);
+          uint8_t* qs = sQ + ln * Cfg::kTileBytes;
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (valid) v = *reinterpret_cast<const uint4*>(qrow + hf * 64 + ch * 8);
-            qv[4 * ch] = v.x;
-            qv[4 * ch + 1] = v.y;
-            qv[4 * ch + 2] = v.z;
-            qv[4 * ch + 3] = v.w;
-          }
-          tmem_st32(tmem + lane_off + Cfg::kColQ + hf * 32, qv);
+          for (int ch = 0; ch < D / 8; ++ch)
+            *reinterpret_cast<uint4*>(qs + (ch / 8) * kPreTile * 128 + sw128_offset(r, (ch % 8) * 8)) =
+                v[ch];
+          fence_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_q[ln]);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_qt);
-        if (valid && begins) {
-          const int n = static_cast<int>((rg.t0 + i + w.nt - 1) / rg.per) - blockIdx.x + 1;
-          p.pre_meta[out_row] = make_int2(blockIdx.x, n);
+        if (valid && begins && (ln == 0 || !split)) {
+          const int over = w.steps() - (n_mine - i);  // steps in later CTAs
+          const int n = over <= 0 ? 1 : 1 + (over + per - 1) / per;
+          p.pre_meta[out_row] = make_int2(blockIdx.x, 2 * n + split);
         }
         m_used = -INFINITY;
         l = 0.f;
+        any = false;
       }
-      // a listed page that is none: its keys are masked (its tile holds zeros)
-      bool bad_page = false;
-      {
-        const int li = w.tile * per + lane;
-        if (lane < per && static_cast<long long>(li) * p.P < w.gr.len) {
-          const int id = p.prefix_pages[static_cast<size_t>(w.j) * p.max_prefix_pages + li];
-          bad_page = id < 0 || id >= p.num_pages;
-        }
-      }
-      if (!(ok = warp_wait(&bar_s[b], (i >> 1) & 1, abort_flag))) break;
-      tc_fence_after();
-      float s[kPreTile];
-#pragma unroll
-      for (int c = 0; c < kPreTile / 32; ++c)
-        tmem_ld32(tmem + lane_off + b * 128 + c * 32, reinterpret_cast<uint32_t*>(s + c * 32));
-      tmem_ld_wait();
-      const int lim = w.gr.len - w.tile * kPreTile;
-      if (lim < kPreTile) {
-#pragma unroll
-        for (int c = 0; c < kPreTile; ++c) s[c] = c < lim ? s[c] : -INFINITY;
-        // values behind the end count 0 times, but 0 times NaN is NaN: zero their rows
-        const int vs = i % Cfg::kNV;
-        if (!(ok = warp_wait(&bar_vf[vs], (i / Cfg::kNV) & 1, abort_flag))) break;
-        if (r >= lim) {
-#pragma unroll
-          for (int hf = 0; hf < Cfg::kHalves; ++hf) {
-            uint4* row = reinterpret_cast<uint4*>(sV + vs * Cfg::kTileBytes + hf * kPreTile * 128 +
-                                                  r * 128);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+      if (mine) {
+        const int tile = w.tile(ln);
+        // a listed page that is none: its keys are masked (its tile holds zeros)
+        bool bad_page = false;
+        {
+          const int li = tile * per_tile + lane;
+          if (lane < per_tile && static_cast<long long>(li) * p.P < w.gr.len) {
+            const int id = p.prefix_pages[static_cast<size_t>(w.j) * p.max_prefix_pages + li];
+            bad_page = id < 0 || id >= p.num_pages;
           }
         }
-        fence_async_smem();
-      }
-      const uint32_t bad = __ballot_sync(0xffffffffu, bad_page);
-      if (bad) {
-        uint32_t drop = 0;
-        for (int k = 0; k < kPreTile / 16; ++k)
-          if ((bad >> (16 * k / p.P)) & 1u) drop |= 1u << k;
-#pragma unroll
-        for (int c = 0; c < kPreTile; ++c) s[c] = ((drop >> (c >> 4)) & 1u) ? -INFINITY : s[c];
-      }
-      float m8[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m8[e] = s[e];
-#pragma unroll
-      for (int c = 8; c < kPreTile; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
-      const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                             fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
-      const bool need = mt > m_used + kRescaleThreshold;
-      const float m_new = need ? mt : m_used;
-      const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
-      if (!first && __any_sync(0xffffffffu, need)) {
-        // PV of the tile before must land before O is rescaled.  S_i's commit implies
-        // that PV_{i-2} is complete and PV_i waits for P_i, so bar_o is in phase i-1
-        // or i here and the parity names PV_{i-1}.
-        if (!(ok = warp_wait(&bar_o, (i - 1) & 1, abort_flag))) break;
+        if (!(ok = warp_wait(&bar_s[ln], n_s & 1, abort_flag))) break;
+        ++n_s;
         tc_fence_after();
+        float s[kPreTile];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_off + Cfg::kColO + c * 32, o);
-          tmem_ld_wait();
+        for (int c = 0; c < kPreTile / 32; ++c)
+          tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(s + c * 32));
+        tmem_ld_wait();
+        const int lim = w.gr.len - tile * kPreTile;
+        if (lim < kPreTile) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(tmem + lane_off + Cfg::kColO + c * 32, o);
+          for (int c = 0; c < kPreTile; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+          // values behind the end count 0 times, but 0 times NaN is NaN: zero their rows
+          if (!(ok = warp_wait(&full[vc % NS], (vc / NS) & 1, abort_flag))) break;
+          if (r >= lim) {
+#pragma unroll
+            for (int hf = 0; hf < Cfg::kHalves; ++hf) {
+              uint4* row = reinterpret_cast<uint4*>(ring + (vc % NS) * Cfg::kTileBytes +
+                                                    hf * kPreTile * 128 + r * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_async_smem();
         }
+        const uint32_t bad = __ballot_sync(0xffffffffu, bad_page);
+        if (bad) {
+          uint32_t drop = 0;
+          for (int k = 0; k < kPreTile / 16; ++k)
+            if ((bad >> ((16 * k) >> lg_p)) & 1u) drop |= 1u << k;
+#pragma unroll
+          for (int c = 0; c < kPreTile; ++c) s[c] = ((drop >> (c >> 4)) & 1u) ? -INFINITY : s[c];
+        }
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = s[e];
+#pragma unroll
+        for (int c = 8; c < kPreTile; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
+        const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
+        const bool need = mt > m_used + kRescaleThreshold;
+        const float m_new = need ? mt : m_used;
+        const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
+        if (any && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(to + c * 32, o);
+          }
+          tmem_st_wait();
+        }
+        any = true;
+        m_used = m_new;
+        const float neg_mref = m_used == -INFINITY ? 0.f : -m_used;
+        float l8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) l8[e] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float p0 = fast_exp2(fmaf(s[32 * q + 2 * c], p.scale_log2, neg_mref));
+            const float p1 = fast_exp2(fmaf(s[32 * q + 2 * c + 1], p.scale_log2, neg_mref));
+            l8[c & 7] += p0 + p1;
+            pk[c] = pack_bf16(p0, p1);
+          }
+          tmem_st16(ts + q * 16, pk);
+        }
+        l = l * alpha + (((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7])));
         tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_p[ln]);
       }
-      m_used = m_new;
-      const float neg_mref = m_used == -INFINITY ? 0.f : -m_used;
-      float l8[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) l8[e] = 0.f;
-      uint32_t pk[kPreTile / 2];
-#pragma unroll
-      for (int c = 0; c < kPreTile / 2; ++c) {
-        const float p0 = fast_exp2(fmaf(s[2 * c], p.scale_log2, neg_mref));
-        const float p1 = fast_exp2(fmaf(s[2 * c + 1], p.scale_log2, neg_mref));
-        l8[c & 7] += p0 + p1;
-        pk[c] = pack_bf16(p0, p1);
-      }
-      l = l * alpha + (((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7])));
-#pragma unroll
-      for (int c = 0; c < kPreTile / 2 / 16; ++c)
-        tmem_st16(tmem + lane_off + b * 128 + c * 16, pk + c * 16);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_p[b]);
 
-      if (i == n_mine - 1 || w.tile == w.nt - 1) {
+      if (i == n_mine - 1 || w.step == w.steps() - 1) {
         // ------------------------------------------------ end of a unit
-        if (!(ok = warp_wait(&bar_fin, n_units & 1, abort_flag))) break;
-        ++n_units;
-        tc_fence_after();
-        const bool whole = begins && w.tile == w.nt - 1;
-        const size_t slot_row = (static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * kPreTile + r;
-        float* od = whole ? p.pre_row_o + out_row * D : p.pre_slot_o + slot_row * D;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const bool whole = begins && w.step == w.steps() - 1;
+        const size_t slot_row =
+            ((static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * 2 + ln) * kPreTile + r;
+        float* od = whole ? p.pre_row_o[split ? ln : 0] + out_row * D : p.pre_slot_o + slot_row * D;
+        if (any) {
+          if (!(ok = warp_wait(&bar_fin[ln], n_units & 1, abort_flag))) break;
+          ++n_units;
+          tc_fence_after();
+          const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_off + Cfg::kColO + c * 32, o);
-          tmem_ld_wait();
-          if (valid)
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_ld_wait();
+            if (valid)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(od + c * 32 + 4 * e) = make_float4(
-                  __uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                  __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4*>(od + c * 32 + 4 * e) = make_float4(
+                    __uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                    __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+          }
         }
         if (valid)
-          *(whole ? p.pre_row_lse + out_row : p.pre_slot_lse + slot_row) =
-              l > 0.f ? m_used + log2f(l) : -INFINITY;
-        tc_fence_before();  // these reads come before the next unit's P and Q
+          *(whole ? p.pre_row_lse[split ? ln : 0] + out_row : p.pre_slot_lse + slot_row) =
+              any && l > 0.f ? m_used + log2f(l) : -INFINITY;
+        tc_fence_before();  // these reads come before the next unit's products
       }
-      w.next(p, i + 1 < n_mine);
+      w.skip(p, 1, i + 1 < n_mine);
     }
     if (!ok) {
       *abort_flag = 1;
@@ -1021,14 +1089,11 @@ __global__ void __launch_bounds__(224, 1)
   tc_fence_before();
   __syncthreads();
   // After an abort, wait (bounded) for TMA loads still landing in shared memory.
-  if (abort_sh && warp == 4 && lane == 0) {
-    for (int i = k_used_sh; i < k_issued_sh; ++i)
-      mbar_wait_drain(&bar_kf[i % Cfg::kNK], (i / Cfg::kNK) & 1);
-    for (int i = v_used_sh; i < v_issued_sh; ++i)
-      mbar_wait_drain(&bar_vf[i % Cfg::kNV], (i / Cfg::kNV) & 1);
-  }
+  if (abort_sh && threadIdx.x == 256)
+    for (int i = max(0, issued_sh - NS); i < issued_sh; ++i)
+      mbar_wait_drain(&full[i % NS], (i / NS) & 1);
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }
@@ -1065,7 +1130,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
   const long long row = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
   const bool active = row < n_rows;
   const int b = active ? static_cast<int>(row / p.Hq) : 0, h = active ? static_cast<int>(row % p.Hq) : 0;
-  int n_pre = 0, pre_row_in = 0;
+  int n_pre = 0, pre_row_in = 0;  // row of its 256-row unit
   if (p.n_groups > 0 && active) {
     const int j = find_group(p, b);
     if (j >= 0) {
@@ -1073,7 +1138,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
       if (b >= gr.lo && b < gr.hi && gr.len > 0) {
         n_pre = 1;
         pre_row_in = static_cast<int>(
-            (static_cast<long long>(b - gr.lo) * p.G + h % p.G) % kPreTile);
+            (static_cast<long long>(b - gr.lo) * p.G + h % p.G) % (2 * kPreTile));
       }
     }
   }
@@ -1086,25 +1151,31 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
     if (p.n_groups == 0 && own.y == 1) own.y = -1;
   }
   const bool work = active && own.y >= 0;
-  const int n = work ? own.y + pre.y : 0;
+  const int split = pre.y & 1, pre_ctas = pre.y >> 1;
+  const int n = work ? own.y + (pre_ctas << split) : 0;
   const int own_row_in = h % p.G % p.own_rows;
-  auto lse_at = [&](int k) {
-    if (k < own.y) {
-      const size_t slot = static_cast<size_t>(own.x + k) * 2 + (k == 0);
-      return own.y == 1 ? p.own_row_lse + row : p.own_slot_lse + slot * p.own_rows + own_row_in;
-    }
-    k -= own.y;
-    const size_t slot = static_cast<size_t>(pre.x + k) * 2 + (k == 0);
-    return pre.y == 1 ? p.pre_row_lse + row : p.pre_slot_lse + slot * kPreTile + pre_row_in;
+  // where part k is: its row in the arrays of O and LSE
+  struct Part {
+    const float* o;
+    const float* lse;
   };
-  auto o_at = [&](int k) {
+  auto part = [&](int k) {
+    Part r;
     if (k < own.y) {
       const size_t slot = static_cast<size_t>(own.x + k) * 2 + (k == 0);
-      return own.y == 1 ? p.own_row_o + row * D : p.own_slot_o + (slot * p.own_rows + own_row_in) * D;
+      const size_t at = own.y == 1 ? row : slot * p.own_rows + own_row_in;
+      r.o = (own.y == 1 ? p.own_row_o : p.own_slot_o) + at * D;
+      r.lse = (own.y == 1 ? p.own_row_lse : p.own_slot_lse) + at;
+    } else {
+      k -= own.y;
+      const int ln = split ? k & 1 : pre_row_in / kPreTile;
+      const int c = k >> split;
+      const size_t slot = (static_cast<size_t>(pre.x + c) * 2 + (c == 0)) * 2 + ln;
+      const size_t at = pre_ctas == 1 ? row : slot * kPreTile + pre_row_in % kPreTile;
+      r.o = (pre_ctas == 1 ? p.pre_row_o[split ? ln : 0] : p.pre_slot_o) + at * D;
+      r.lse = (pre_ctas == 1 ? p.pre_row_lse[split ? ln : 0] : p.pre_slot_lse) + at;
     }
-    k -= own.y;
-    const size_t slot = static_cast<size_t>(pre.x + k) * 2 + (k == 0);
-    return pre.y == 1 ? p.pre_row_o + row * D : p.pre_slot_o + (slot * kPreTile + pre_row_in) * D;
+    return r;
   };
   const int w = warp % W, sub = lane / TPR, d4 = (lane % TPR) * 4;
   // each warp (or part of one) its share of the parts, four loads of LSE and O at
@@ -1121,8 +1192,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
       const int k = k0 + i * W * PPW;
       lk[i] = -INFINITY;
       if (k < n) {
-        lk[i] = *lse_at(k);
-        y[i] = *reinterpret_cast<const float4*>(o_at(k) + d4);
+        const Part r = part(k);
+        lk[i] = *r.lse;
+        y[i] = *reinterpret_cast<const float4*>(r.o + d4);
       }
     }
     const float m = fmaxf(fmaxf(fmaxf(lk[0], lk[1]), fmaxf(lk[2], lk[3])), top);
@@ -1218,12 +1290,12 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   p->own_rows = own_unit_rows(G);
   p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
   const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D, p->own_rows)) * p->own_rows;
-  const size_t pre_rows = 2 * static_cast<size_t>(sms) * kPreTile;
+  const size_t pre_rows = 4 * static_cast<size_t>(sms) * kPreTile;
   p->own_meta = reinterpret_cast<int2*>(take(static_cast<size_t>(n_seqs) * Hkv * p->row_tiles * 8));
   p->own_slot_o = reinterpret_cast<float*>(take(own_rows * D * 4));
   p->own_slot_lse = reinterpret_cast<float*>(take(own_rows * 4));
-  p->own_row_o = p->own_row_lse = p->pre_slot_o = p->pre_slot_lse = p->pre_row_o = p->pre_row_lse =
-      nullptr;
+  p->own_row_o = p->own_row_lse = p->pre_slot_o = p->pre_slot_lse = nullptr;
+  p->pre_row_o[0] = p->pre_row_o[1] = p->pre_row_lse[0] = p->pre_row_lse[1] = nullptr;
   p->pre_meta = nullptr;
   if (n_groups > 0) {
     p->own_row_o = reinterpret_cast<float*>(take(rows * D * 4));
@@ -1231,8 +1303,10 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
     p->pre_meta = reinterpret_cast<int2*>(take(rows * 8));
     p->pre_slot_o = reinterpret_cast<float*>(take(pre_rows * D * 4));
     p->pre_slot_lse = reinterpret_cast<float*>(take(pre_rows * 4));
-    p->pre_row_o = reinterpret_cast<float*>(take(rows * D * 4));
-    p->pre_row_lse = reinterpret_cast<float*>(take(rows * 4));
+    for (int ln = 0; ln < 2; ++ln) {
+      p->pre_row_o[ln] = reinterpret_cast<float*>(take(rows * D * 4));
+      p->pre_row_lse[ln] = reinterpret_cast<float*>(take(rows * 4));
+    }
   }
   return at;
 }
@@ -1270,7 +1344,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   if (p.n_groups > 0) {
     if (!kv_map(&map, pool, p.P, 1)) return OOMB_ERR_CUDA;
     cfg.gridDim = dim3(sms);
-    cfg.blockDim = dim3(224);
+    cfg.blockDim = dim3(kPreThreads);
     cfg.dynamicSmemBytes = PreCfg<D>::kSmem;
     cfg.numAttrs = 0;
     e = cudaLaunchKernelEx(&cfg, prefix_kernel<D>, p, map);
