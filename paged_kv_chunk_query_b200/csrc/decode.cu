@@ -698,6 +698,31 @@ __device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
   return d;
 }
 
+// Two fp32 values at once, and the largest of three (sm_100).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -729,7 +754,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* ring = sQ + 2 * Cfg::kTileBytes;
   __shared__ uint64_t full[NS], empty[NS];
-  __shared__ uint64_t bar_q[2], bar_s[2], bar_p[2], bar_fin[2], bar_drain;
+  __shared__ uint64_t bar_q[2], bar_s[2], bar_p[2][2], bar_fin[2], bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh;
   const int warp = warp_id(), lane = lane_id();
@@ -744,7 +769,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_q[i], 4);
       mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_p[i], 4);
+      mbar_init(&bar_p[i][0], 4);
+      mbar_init(&bar_p[i][1], 4);
       mbar_init(&bar_fin[i], 1);
     }
     mbar_init(&bar_drain, 1);
@@ -856,18 +882,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         return true;
       };
       auto pv = [&](int ln, int c, bool fresh, bool release, bool last) {  // O += P V
-        if (!warp_wait(&bar_p[ln], (n_s[ln] - 1) & 1, abort_flag) || !wait_tile(c)) return false;
-        tc_fence_after();
+        if (!wait_tile(c)) return false;
         const uint32_t b = v_lo + (c % NS) * kTile16;
-        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kPreTile / 16; ++kk)
-            umma_ts(tmem + 256 + ln * 128, tmem + ln * 128 + kk * 8, desc64(b + kk * 128, kHi),
-                    idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
-          if (release) umma_commit(&empty[c % NS]);
-          if (last) umma_commit(&bar_fin[ln]);
+        for (int half = 0; half < 2; ++half) {
+          if (!warp_wait(&bar_p[ln][half], (n_s[ln] - 1) & 1, abort_flag)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k2 = 0; k2 < kPreTile / 32; ++k2) {
+              const int kk = half * (kPreTile / 32) + k2;
+              umma_ts(tmem + 256 + ln * 128, tmem + ln * 128 + kk * 8, desc64(b + kk * 128, kHi),
+                      idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+            }
+            if (half == 1) {
+              if (release) umma_commit(&empty[c % NS]);
+              if (last) umma_commit(&bar_fin[ln]);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
         return true;
       };
       for (int left = n_mine; ok && left > 0;) {
@@ -1002,13 +1036,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
           for (int c = 0; c < kPreTile; ++c) s[c] = ((drop >> (c >> 4)) & 1u) ? -INFINITY : s[c];
         }
+        // eight chains of maxima of three
         float m8[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = s[e];
+        for (int e = 0; e < 8; ++e) m8[e] = max3(s[e], s[8 + e], s[16 + e]);
 #pragma unroll
-        for (int c = 8; c < kPreTile; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
-        const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
+        for (int c = 24; c < kPreTile; c += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            m8[e] = c + 8 < kPreTile ? max3(m8[e], s[c + e], s[c + 8 + e]) : fmaxf(m8[e], s[c + e]);
+        const float mt = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
+                              fmaxf(m8[6], m8[7])) * p.scale_log2;
         const bool need = mt > m_used + kRescaleThreshold;
         const float m_new = need ? mt : m_used;
         const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
@@ -1027,26 +1065,32 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         any = true;
         m_used = m_new;
         const float neg_mref = m_used == -INFINITY ? 0.f : -m_used;
-        float l8[8];
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), neg2 = pack2(neg_mref, neg_mref);
+        uint64_t l2[4] = {0, 0, 0, 0};
+        // P in two halves: the first half's product runs while the second is computed
 #pragma unroll
-        for (int e = 0; e < 8; ++e) l8[e] = 0.f;
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
+          for (int q = 2 * half; q < 2 * half + 2; ++q) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float p0 = fast_exp2(fmaf(s[32 * q + 2 * c], p.scale_log2, neg_mref));
-            const float p1 = fast_exp2(fmaf(s[32 * q + 2 * c + 1], p.scale_log2, neg_mref));
-            l8[c & 7] += p0 + p1;
-            pk[c] = pack_bf16(p0, p1);
+            for (int c = 0; c < 16; ++c) {
+              float x0, x1;
+              unpack2(fma2(pack2(s[32 * q + 2 * c], s[32 * q + 2 * c + 1]), scale2, neg2), x0, x1);
+              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+              l2[c & 3] = add2(l2[c & 3], pack2(p0, p1));
+              pk[c] = pack_bf16(p0, p1);
+            }
+            tmem_st16(ts + q * 16, pk);
           }
-          tmem_st16(ts + q * 16, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_p[ln][half]);
         }
-        l = l * alpha + (((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7])));
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_p[ln]);
+        float la, lb;
+        unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), la, lb);
+        l = l * alpha + (la + lb);
       }
 
       if (i == n_mine - 1 || w.step == w.steps() - 1) {
