@@ -698,6 +698,20 @@ __device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
   return d;
 }
 
+// A place in a ring of NS slots and the parity of its barriers' phase.
+template <int NS>
+struct RingPos {
+  int slot;
+  uint32_t par;
+  __device__ __forceinline__ RingPos at(int n) const {  // n <= NS places on
+    RingPos r{slot + n, par};
+    if (r.slot >= NS) {
+      r.slot -= NS;
+      r.par ^= 1;
+    }
+    return r;
+  }
+};
 // Two fp32 values at once, and the largest of three (sm_100).
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t d;
@@ -860,33 +874,31 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const uint32_t v_lo = (smem_u32(ring) >> 4) | (((kPreTile * 128u) >> 4) << 16);
       PreWalk w;
       w.start(p, rg);
-      int n_s[2] = {0, 0}, n_units[2] = {0, 0};  // S products and units of a lane so far
-      int cnt = 0;                               // tiles of the ring before this step
+      uint32_t par_p[2] = {1, 1}, par_q[2] = {1, 1};  // of a lane's latest P and queries
+      RingPos<NS> pos{0, 0};                          // the step's first tile
       bool ok = true;
-      auto wait_tile = [&](int c) { return warp_wait(&full[c % NS], (c / NS) & 1, abort_flag); };
-      auto qk = [&](int ln, int c, bool release) {  // S = Q K^T
-        if (!wait_tile(c)) return false;
+      auto qk = [&](int ln, RingPos<NS> k, bool arrived, bool release) {  // S = Q K^T
+        if (!arrived) ok = ok && warp_wait(&full[k.slot], k.par, abort_flag);
         tc_fence_after();
-        const uint32_t a = q_lo + ln * kTile16, b = k_lo + (c % NS) * kTile16;
+        const uint32_t a = q_lo + ln * kTile16, b = k_lo + k.slot * kTile16;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk / 4) * (kPreTile * 128) + (kk % 4) * 32) >> 4;
             umma_ss(tmem + ln * 128, desc64(a + off, kHi), desc64(b + off, kHi), idesc_s, kk > 0);
           }
-          if (release) umma_commit(&empty[c % NS]);
           umma_commit(&bar_s[ln]);
+          if (release) umma_commit(&empty[k.slot]);
         }
         __syncwarp();
-        ++n_s[ln];
-        return true;
+        par_p[ln] ^= 1;
       };
-      auto pv = [&](int ln, int c, bool fresh, bool release, bool last) {  // O += P V
-        if (!wait_tile(c)) return false;
-        const uint32_t b = v_lo + (c % NS) * kTile16;
+      auto pv = [&](int ln, RingPos<NS> v, bool arrived, bool fresh, bool release, bool last) {
+        if (!arrived) ok = ok && warp_wait(&full[v.slot], v.par, abort_flag);
+        const uint32_t b = v_lo + v.slot * kTile16;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!warp_wait(&bar_p[ln][half], (n_s[ln] - 1) & 1, abort_flag)) return false;
+        for (int half = 0; half < 2; ++half) {  // O += P V
+          ok = ok && warp_wait(&bar_p[ln][half], par_p[ln], abort_flag);
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -896,13 +908,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                       idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
             }
             if (half == 1) {
-              if (release) umma_commit(&empty[c % NS]);
+              if (release) umma_commit(&empty[v.slot]);
               if (last) umma_commit(&bar_fin[ln]);
             }
           }
           __syncwarp();
         }
-        return true;
       };
       for (int left = n_mine; ok && left > 0;) {
         // a unit: its steps here, whether lane 1 has a tile of its own, and in the last step
@@ -913,20 +924,37 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         left -= here;
         // the lanes' queries come when the old unit's O has been read
         const bool two0 = !(odd && here == 1);
-        for (int ln = 0; ok && ln < 1 + two0; ++ln)
-          ok = warp_wait(&bar_q[ln], n_units[ln]++ & 1, abort_flag);
-        ok = ok && qk(0, cnt, split || !two0);
-        ok = ok && (!two0 || qk(1, cnt + split, true));
-        for (int i = 0; ok && i < here; ++i) {
-          const bool more = i + 1 < here;
-          const bool two = more || !odd, ntwo = more && (i + 2 < here || !odd);
-          const bool extra = split && two, nextra = split && ntwo;
-          const int va = cnt + 1 + extra, vb = va + extra;
-          cnt += 2 + 2 * extra;
-          ok = pv(0, va, i == 0, extra || !two, !more);
-          ok = ok && (!more || qk(0, cnt, nextra || !ntwo));
-          ok = ok && (!two || pv(1, vb, i == 0, true, !ntwo));
-          ok = ok && (!ntwo || qk(1, cnt + nextra, true));
+        for (int ln = 0; ln < 1 + two0; ++ln) {
+          par_q[ln] ^= 1;
+          ok = ok && warp_wait(&bar_q[ln], par_q[ln], abort_flag);
+        }
+        if (!ok) break;
+        if (!split) {
+          // both lanes take the same tiles
+          qk(0, pos, false, false);
+          qk(1, pos, true, true);
+          for (int i = 0; ok && i < here; ++i) {
+            const bool last = i + 1 == here;
+            const RingPos<NS> v = pos.at(1);
+            pos = pos.at(2);
+            pv(0, v, false, i == 0, false, last);
+            if (!last) qk(0, pos, false, false);
+            pv(1, v, true, i == 0, true, last);
+            if (!last) qk(1, pos, true, true);
+          }
+        } else {
+          // a tile each, lane 1 perhaps none in the last step
+          qk(0, pos, false, true);
+          if (two0) qk(1, pos.at(1), false, true);
+          for (int i = 0; ok && i < here; ++i) {
+            const bool more = i + 1 < here, two = more || !odd, ntwo = more && (i + 2 < here || !odd);
+            const RingPos<NS> v = pos.at(1 + two);
+            pos = pos.at(2 + 2 * two);
+            pv(0, v, false, i == 0, true, !more);
+            if (more) qk(0, pos, false, true);
+            if (two) pv(1, v.at(1), false, i == 0, true, !ntwo);
+            if (ntwo) qk(1, pos.at(1), false, true);
+          }
         }
         w.skip(p, here, left > 0);
       }
@@ -1104,17 +1132,34 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           ++n_units;
           tc_fence_after();
           const float inv = l > 0.f ? 1.f / l : 0.f;
+          // half a row at a time through the warp's part of its query tile, which nothing
+          // reads any more: D / 8 lanes then write a row's half together
+          constexpr int LPR = D / 8, RPI = 32 / LPR;
+          const unsigned long long addr = valid ? reinterpret_cast<unsigned long long>(od) : 0ull;
+          float4* stage = reinterpret_cast<float4*>(sQ + ln * Cfg::kTileBytes +
+                                                    (warp & 3) * 32 * D * 2);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + c * 32, o);
-            tmem_ld_wait();
-            if (valid)
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + half * (D / 2) + c * 16, o);
+              tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<float4*>(od + c * 32 + 4 * e) = make_float4(
+              for (int e = 0; e < 4; ++e)
+                stage[lane * LPR + ((4 * c + e) ^ (lane % LPR))] = make_float4(
                     __uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                     __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int it = 0; it < 32 / RPI; ++it) {
+              const int sub = it * RPI + lane / LPR, ch = lane % LPR;
+              const unsigned long long a = __shfl_sync(0xffffffffu, addr, sub);
+              const float4 x = stage[sub * LPR + (ch ^ (sub % LPR))];
+              if (a) *reinterpret_cast<float4*>(a + (half * LPR + ch) * 16) = x;
+            }
+            __syncwarp();
           }
         }
         if (valid)
