@@ -52,7 +52,8 @@ struct DecodeParams {
   uint32_t* status;
   int n_seqs, Hq, Hkv, G, P, max_pages, n_groups, max_prefix_pages, num_pages;
   int own_rows;   // query heads of a unit of own_kernel: 8 or 16
-  int row_tiles;  // its units per KV head
+  int row_tiles;  // a sequence's units per KV head there
+  int pre_in_own; // the prefixes are units of own_kernel too
   float scale_log2;
   // Workspace.  Part results are normalised O (fp32) and base-2 LSE.
   // own_meta [unit] {first CTA, CTAs}; slots [2 CTA + (0: begins before, 1: ends
@@ -217,7 +218,8 @@ struct OwnCfg {
 struct TileInfo {
   int lim;    // valid keys of the tile, at most kOwnTile
   int bad;    // bit w: the page of keys [16 w, 16 w + 16) is none
-  int flags;  // 1: first tile of the unit in this CTA, 2: last one, 4: whole unit, 8: it begins here
+  int flags;  // 1: first tile of the unit in this CTA, 2: last one, 4: whole unit, 8: it begins
+              // here, 16: of a prefix
   int b, h0, rows;  // the unit: sequence, first query head, query heads
 };
 
@@ -233,12 +235,54 @@ struct TileInfo {
 // tiles by TMA (K and V of a page and head are neighbours in the pool: one box of
 // both per 64 columns).  The number of barriers does not depend on what is found, so
 // a wait that gives up leaves nobody behind.
+//
+// PRE: the prefixes' keys are units too, of up to kRows rows (sequence, query head)
+// of a group; items [0, n_groups) are groups, the others sequences.  A sequence is
+// the item of its own G rows.
 constexpr int kOwnThreads = 160;
-template <int D, int NT>
+template <bool PRE, int ROWS>
+struct OwnItem {
+  const int32_t* table;  // its pages
+  int len;
+  int lo, rows;          // first sequence, rows per KV head
+  int nt, row_tiles;     // tiles, units per KV head
+  __device__ __forceinline__ void set(const DecodeParams& p, int i, int raw_len, int g0, int g1,
+                                      uint32_t* status) {
+    if (PRE && i < p.n_groups) {
+      lo = min(max(g0, 0), p.n_seqs);
+      const int hi = min(max(g1, lo), p.n_seqs);
+      if ((lo != g0 || hi != g1) && status) atomicOr(status, OOMB_DEV_BAD_COUNT);
+      len = checked_len(raw_len, p.max_prefix_pages, p.P, status);
+      table = p.prefix_pages + static_cast<size_t>(i) * p.max_prefix_pages;
+      rows = (hi - lo) * p.G;
+      nt = (len + kOwnTile - 1) / kOwnTile;
+      row_tiles = (rows + ROWS - 1) / ROWS;
+    } else {
+      lo = PRE ? i - p.n_groups : i;
+      len = checked_len(raw_len, p.max_pages, p.P, status);
+      table = p.page_tables + static_cast<size_t>(lo) * p.max_pages;
+      rows = p.G;
+      nt = own_tiles(len);
+      row_tiles = p.row_tiles;
+    }
+  }
+  __device__ __forceinline__ void load(const DecodeParams& p, int i, uint32_t* status) {
+    if (PRE && i < p.n_groups)
+      set(p, i, p.prefix_lens[i], p.group_start[i], p.group_start[i + 1], status);
+    else
+      set(p, i, p.seq_lens[PRE ? i - p.n_groups : i], 0, 0, status);
+  }
+  __device__ __forceinline__ long long weight(const DecodeParams& p) const {
+    return static_cast<long long>(nt) * row_tiles * p.Hkv;
+  }
+};
+
+template <int D, int NT, bool PRE>
 __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
     own_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kvmap) {
   using Cfg = OwnCfg<D, NT>;
   constexpr int kRows = Cfg::kRows;
+  using Item = OwnItem<PRE, kRows>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -249,6 +293,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
   // of a tile: maxima per warp and whether they move the running ones; of a unit: sums
   __shared__ __align__(16) float sm[2][4][kRows], sl[2][4][kRows];
   __shared__ __align__(16) int moved[2][4];
+  __shared__ int out_rows[PRE ? Cfg::kStages : 1][kRows];  // sequence x Hq + head of a unit's rows
   __shared__ int abort_sh, issued_sh, used_sh;
   const int warp = warp_id(), lane = lane_id();
   volatile int* abort_flag = &abort_sh;
@@ -266,11 +311,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
   for (int i = threadIdx.x * 16; i < Cfg::kStages * Cfg::kQBytes; i += kOwnThreads * 16)
     *reinterpret_cast<uint4*>(sq + i) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
-  const int units_per_seq = p.Hkv * p.row_tiles;
-  const Range rg = find_range<kOwnThreads>(p.n_seqs, [&](int b, bool note) {
-    const int len = checked_len(p.seq_lens[b], p.max_pages, p.P,
-                                note && blockIdx.x == 0 ? p.status : nullptr);
-    return static_cast<long long>(own_tiles(len)) * units_per_seq;
+  const int n_items = (PRE ? p.n_groups : 0) + p.n_seqs;
+  const Range rg = find_range<kOwnThreads>(n_items, [&](int i, bool note) {
+    Item it;
+    it.load(p, i, note && blockIdx.x == 0 ? p.status : nullptr);
+    return it.weight(p);
   });
   const int n_mine = static_cast<int>(rg.t1 - rg.t0);
 
@@ -282,100 +327,123 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
     const uint32_t box_bytes = 2u * R * 128;
     const int s = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;  // this lane's box
     const int per = static_cast<int>(rg.per);
-    int b = rg.item, len = 0, nt = 1, tile = 0, g = 0, rt = 0, first_id = -1, ids = 0, issued = 0;
-    // the next sequence's length and first page ids, under way while this one's tiles are
-    int next_len = 0, next_ids = -1;
+    Item it;
+    int item = rg.item, tile = 0, g = 0, rt = 0, first_id = -1, ids = 0, issued = 0;
+    // the next item's length (and group) and first page ids, under way while this one's
+    // tiles are
+    int next_len = 0, next_g0 = 0, next_g1 = 0, next_ids = -1;
     auto look_ahead = [&] {
-      if (b + 1 < p.n_seqs) {
-        next_len = p.seq_lens[b + 1];
-        if (lane < p.max_pages)
-          next_ids = p.page_tables[static_cast<size_t>(b + 1) * p.max_pages + lane];
+      const int i = item + 1;
+      if (i >= n_items) return;
+      const bool group = PRE && i < p.n_groups;
+      if (group) {
+        next_len = p.prefix_lens[i];
+        next_g0 = p.group_start[i];
+        next_g1 = p.group_start[i + 1];
+        if (lane < p.max_prefix_pages)
+          next_ids = p.prefix_pages[static_cast<size_t>(i) * p.max_prefix_pages + lane];
+      } else {
+        const int b = PRE ? i - p.n_groups : i;
+        next_len = p.seq_lens[b];
+        if (lane < p.max_pages) next_ids = p.page_tables[static_cast<size_t>(b) * p.max_pages + lane];
       }
     };
-    int2* meta = p.own_meta;  // of the current unit
     if (n_mine > 0) {
-      len = checked_len(p.seq_lens[b], p.max_pages, p.P, nullptr);
+      it.load(p, item, nullptr);
       look_ahead();
-      nt = own_tiles(len);
       const long long off = rg.t0 - rg.item_at;
-      const int u = static_cast<int>(fast_div(off, nt));
-      tile = static_cast<int>(off - static_cast<long long>(u) * nt);
-      g = u / p.row_tiles;
-      rt = u - g * p.row_tiles;
-      meta += static_cast<size_t>(b) * units_per_seq + u;
+      const int u = static_cast<int>(fast_div(off, it.nt));
+      tile = static_cast<int>(off - static_cast<long long>(u) * it.nt);
+      g = u / it.row_tiles;
+      rt = u - g * it.row_tiles;
     }
     for (int i = 0; i < n_mine; ++i) {
       const int st = i % Cfg::kStages;
-      const bool first = i == 0 || tile == 0, last = i == n_mine - 1 || tile == nt - 1;
+      const bool first = i == 0 || tile == 0, last = i == n_mine - 1 || tile == it.nt - 1;
       const int key0 = tile * kOwnTile;
       // 32 page ids at a time, one per lane
       const int pg0 = key0 >> lg_p;
       if (first_id < 0 || pg0 < first_id || pg0 + slots > first_id + 32) {
         first_id = pg0;
         const int at = pg0 + lane;
-        ids = at * static_cast<long long>(p.P) < len
-                  ? p.page_tables[static_cast<size_t>(b) * p.max_pages + at]
-                  : -1;
+        ids = at * static_cast<long long>(p.P) < it.len ? it.table[at] : -1;
       }
       const int page = __shfl_sync(0xffffffffu, ids, (pg0 - first_id + s) & 31);
       const int row0 = key0 + (s << lg_r);  // first token of the box
-      const bool here = s < slots && row0 < len;
+      const bool here = s < slots && row0 < it.len;
       const bool good = here && page >= 0 && page < p.num_pages;
       const unsigned goods = __ballot_sync(0xffffffffu, good);
       unsigned bad = 0;
       if (goods != __ballot_sync(0xffffffffu, here)) {
         for (int k = 0; k < 4; ++k)  // keys [16 k, 16 k + 16)
-          if (key0 + 16 * k < len && !((goods >> (((16 * k) >> lg_r) * Cfg::kHalves)) & 1u))
+          if (key0 + 16 * k < it.len && !((goods >> (((16 * k) >> lg_r) * Cfg::kHalves)) & 1u))
             bad |= 1u << k;
         if (here && !good && hf == 0 && g == 0 && rt == 0) atomicOr(p.status, OOMB_DEV_BAD_PAGE);
       }
-      const int h0 = g * p.G + rt * kRows, rows = min(kRows, p.G - rt * kRows);
-      bool ok = true;
-      if (lane == 0) {
-        ok = mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, abort_flag);
-        if (ok) {
-          // the unit's first tile is this CTA's if it is not further back than its range
-          const bool begins = i >= tile, ends = tile == nt - 1;
-          TileInfo t;
-          t.lim = min(kOwnTile, len - key0);
-          t.bad = static_cast<int>(bad);
-          t.flags = (first ? 1 : 0) | (last ? 2 : 0) | (begins && ends ? 4 : 0) | (begins ? 8 : 0);
-          t.b = b;
-          t.h0 = h0;
-          t.rows = rows;
-          info[st] = t;
-          mbar_arrive_expect_tx(&full[st], __popc(goods) * box_bytes + (first ? rows * D * 2 : 0));
-        }
+      // the unit's rows: row r of the item is head r % G of sequence lo + r / G
+      const int r0 = rt * kRows, rows = min(kRows, it.rows - r0);
+      int seq = it.lo, head = g * p.G + r0 + lane;
+      if (PRE && item < p.n_groups) {
+        const int d = (r0 + lane) / p.G;
+        seq += d;
+        head -= d * p.G;
       }
+      bool ok = true;
+      if (lane == 0) ok = mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       ++issued;
+      if (PRE) {
+        if (last && lane < rows) out_rows[st][lane] = seq * p.Hq + head;
+        __syncwarp();
+      }
+      if (lane == 0) {
+        // the unit's first tile is this CTA's if it is not further back than its range
+        const bool begins = i >= tile, ends = tile == it.nt - 1;
+        TileInfo t;
+        t.lim = min(kOwnTile, it.len - key0);
+        t.bad = static_cast<int>(bad);
+        t.flags = (first ? 1 : 0) | (last ? 2 : 0) | (begins && ends ? 4 : 0) | (begins ? 8 : 0) |
+                  (PRE && item < p.n_groups ? 16 : 0);
+        t.b = seq;
+        t.h0 = head;
+        t.rows = rows;
+        info[st] = t;
+        mbar_arrive_expect_tx(&full[st], __popc(goods) * box_bytes + (first ? rows * D * 2 : 0));
+      }
+      __syncwarp();
       if (good)
         tma_load_4d(ring + st * Cfg::kTileBytes + (hf * slots + s) * box_bytes, &kvmap, &full[st],
                     hf * 64, row0 & (p.P - 1), 2 * g, page);
       if (first && lane < rows)
-        bulk_load(sq + st * Cfg::kQBytes + lane * Cfg::kQRow,
-                  p.q + b * p.q_stride + (h0 + lane) * D, D * 2, &full[st]);
-      if (tile == 0 && lane == 0) {
-        const int over = nt - (n_mine - i);  // its tiles in later CTAs
-        *meta = make_int2(blockIdx.x, over <= 0 ? 1 : 1 + (over + per - 1) / per);
+        bulk_load(sq + st * Cfg::kQBytes + lane * Cfg::kQRow, p.q + seq * p.q_stride + head * D, D * 2,
+                  &full[st]);
+      if (tile == 0) {
+        const int over = it.nt - (n_mine - i);  // its tiles in later CTAs
+        const int n = over <= 0 ? 1 : 1 + (over + per - 1) / per;
+        if (PRE && item < p.n_groups) {
+          if (lane < rows) p.pre_meta[static_cast<size_t>(seq) * p.Hq + head] = make_int2(blockIdx.x, 2 * n);
+        } else if (lane == 0) {
+          p.own_meta[(static_cast<size_t>(it.lo) * p.Hkv + g) * p.row_tiles + rt] =
+              make_int2(blockIdx.x, n);
+        }
       }
       // next tile
-      if (++tile == nt) {
+      if (++tile == it.nt) {
         tile = 0;
-        ++meta;
-        if (++rt == p.row_tiles) {
+        if (++rt == it.row_tiles) {
           rt = 0;
           ++g;
         }
         if (g == p.Hkv) {
           g = 0;
-          ++b;
-          len = checked_len(next_len, p.max_pages, p.P, nullptr);
-          nt = own_tiles(len);
-          first_id = 0;
-          ids = next_ids;
-          look_ahead();
+          do {  // groups without keys or rows have no tiles
+            if (++item >= n_items) break;
+            it.set(p, item, next_len, next_g0, next_g1, nullptr);
+            first_id = 0;
+            ids = next_ids;
+            look_ahead();
+          } while (it.weight(p) == 0);
         }
       }
     }
@@ -563,11 +631,12 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (!(PRE && (t.flags & 2)) && lane == 0) mbar_arrive(&empty[st]);
       if (!(t.flags & 2)) continue;
 
       // ---------------------------------------------------------- end of a unit
-      const bool whole = t.flags & 4, direct = whole && p.n_groups == 0;
+      const bool whole = t.flags & 4, direct = !PRE && whole && p.n_groups == 0;
+      const bool pre = t.flags & 16;
       const size_t row0 = static_cast<size_t>(t.b) * p.Hq + t.h0;
       const size_t slot0 = (static_cast<size_t>(blockIdx.x) * 2 + (t.flags & 8 ? 1 : 0)) * kRows;
 #pragma unroll
@@ -587,8 +656,14 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
           for (int e = 0; e < 2; ++e) {
             const int row = n * 8 + hd + e;
             if (row >= t.rows) continue;
-            if (!direct) (whole ? p.own_row_lse + row0 : p.own_slot_lse + slot0)[row] = lse[e];
-            else if (p.lse) p.lse[row0 + row] = kLn2 * lse[e];
+            if (direct) {
+              if (p.lse) p.lse[row0 + row] = kLn2 * lse[e];
+            } else if (!whole) {
+              p.own_slot_lse[slot0 + row] = lse[e];
+            } else {
+              (PRE && pre ? p.pre_row_lse[0] : p.own_row_lse)[PRE ? out_rows[st][row] : row0 + row] =
+                  lse[e];
+            }
           }
         }
         if (direct) {
@@ -604,19 +679,27 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
             }
           }
         } else {
-          float* dst = (whole ? p.own_row_o + row0 * D : p.own_slot_o + slot0 * D) +
-                       (n * 8 + hd) * D + col0 + lane / 4;
 #pragma unroll
-          for (int c = 0; c < MT; ++c)
+          for (int e = 0; e < 2; ++e) {
+            const int row = n * 8 + hd + e;
+            if (row >= t.rows) continue;
+            float* dst = !whole ? p.own_slot_o + (slot0 + row) * D
+                                : (PRE && pre ? p.pre_row_o[0] : p.own_row_o) +
+                                      (PRE ? static_cast<size_t>(out_rows[st][row]) : row0 + row) * D;
+            dst += col0 + lane / 4;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (n * 8 + hd + e < t.rows) {
-                dst[e * D + 16 * c] = acc[n][c][e] * (e ? i1 : i0);
-                dst[e * D + 16 * c + 8] = acc[n][c][e + 2] * (e ? i1 : i0);
-              }
+            for (int c = 0; c < MT; ++c) {
+              dst[16 * c] = acc[n][c][e] * (e ? i1 : i0);
+              dst[16 * c + 8] = acc[n][c][e + 2] * (e ? i1 : i0);
+            }
+          }
         }
       }
       ++n_units;
+      if (PRE) {  // out_rows of this stage has been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+      }
     }
     if (threadIdx.x == 0) used_sh = used;
   }
@@ -1132,12 +1215,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           ++n_units;
           tc_fence_after();
           const float inv = l > 0.f ? 1.f / l : 0.f;
-          // half a row at a time through the warp's part of its query tile, which nothing
-          // reads any more: D / 8 lanes then write a row's half together
+          // half a row at a time through the place of the warp's own queries, which nothing
+          // reads any more (other warps may be writing the next unit's into theirs): D / 8
+          // lanes then write a row's half together
           constexpr int LPR = D / 8, RPI = 32 / LPR;
           const unsigned long long addr = valid ? reinterpret_cast<unsigned long long>(od) : 0ull;
-          float4* stage = reinterpret_cast<float4*>(sQ + ln * Cfg::kTileBytes +
-                                                    (warp & 3) * 32 * D * 2);
+          uint8_t* qs = sQ + ln * Cfg::kTileBytes;
+          auto stage = [&](int row, int ch) {  // 16-byte chunk of a row of the warp
+            return reinterpret_cast<float4*>(qs + (ch / 8) * kPreTile * 128 +
+                                             sw128_offset((warp & 3) * 32 + row, (ch % 8) * 8));
+          };
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -1147,7 +1234,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                stage[lane * LPR + ((4 * c + e) ^ (lane % LPR))] = make_float4(
+                *stage(lane, 4 * c + e) = make_float4(
                     __uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                     __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
             }
@@ -1156,7 +1243,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             for (int it = 0; it < 32 / RPI; ++it) {
               const int sub = it * RPI + lane / LPR, ch = lane % LPR;
               const unsigned long long a = __shfl_sync(0xffffffffu, addr, sub);
-              const float4 x = stage[sub * LPR + (ch ^ (sub % LPR))];
+              const float4 x = *stage(sub, ch);
               if (a) *reinterpret_cast<float4*>(a + (half * LPR + ch) * 16) = x;
             }
             __syncwarp();
@@ -1257,12 +1344,19 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
       r.lse = (own.y == 1 ? p.own_row_lse : p.own_slot_lse) + at;
     } else {
       k -= own.y;
-      const int ln = split ? k & 1 : pre_row_in / kPreTile;
+      const int ln = split ? k & 1 : p.pre_in_own ? 0 : pre_row_in / kPreTile;
       const int c = k >> split;
-      const size_t slot = (static_cast<size_t>(pre.x + c) * 2 + (c == 0)) * 2 + ln;
-      const size_t at = pre_ctas == 1 ? row : slot * kPreTile + pre_row_in % kPreTile;
-      r.o = (pre_ctas == 1 ? p.pre_row_o[split ? ln : 0] : p.pre_slot_o) + at * D;
-      r.lse = (pre_ctas == 1 ? p.pre_row_lse[split ? ln : 0] : p.pre_slot_lse) + at;
+      size_t slot = static_cast<size_t>(pre.x + c) * 2 + (c == 0);
+      if (!p.pre_in_own) slot = slot * 2 + ln;
+      const size_t at = pre_ctas == 1   ? static_cast<size_t>(row)
+                        : p.pre_in_own ? slot * p.own_rows + pre_row_in % p.own_rows
+                                       : slot * kPreTile + pre_row_in % kPreTile;
+      r.o = (pre_ctas == 1  ? p.pre_row_o[split ? ln : 0]
+             : p.pre_in_own ? p.own_slot_o
+                            : p.pre_slot_o) + at * D;
+      r.lse = (pre_ctas == 1  ? p.pre_row_lse[split ? ln : 0]
+               : p.pre_in_own ? p.own_slot_lse
+                              : p.pre_slot_lse) + at;
     }
     return r;
   };
@@ -1358,8 +1452,17 @@ bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_gr
          static_cast<int64_t>(n_seqs) * Hq <= INT32_MAX;
 }
 
-// Query heads of a unit of own_kernel: one column of 8, or two.
-int own_unit_rows(int G) { return G <= 8 ? 8 : 16; }
+// Prefix groups of few rows (sequences x query heads per KV head, on average) are units of
+// own_kernel: prefix_kernel takes 128 rows' time for them, and one more launch.  Both
+// ways, own_kernel first: 12 groups of 4 x 7 rows behind 1200 tokens (d = 128) 24.6 and
+// 28.7 us, behind 4000 54 and 51 us; 64 x 7 rows, 500 tokens 27 and 39 us; 30 x 35
+// rows, 2000 tokens 92 and 57 us.
+constexpr int kFewRows = 32;
+bool prefixes_in_own(int n_seqs, int G, int n_groups) {
+  return n_groups > 0 && static_cast<int64_t>(n_seqs) * G <= static_cast<int64_t>(kFewRows) * n_groups;
+}
+// Rows of a unit of own_kernel: one column of 8, or two.
+int own_unit_rows(int G, bool pre) { return G <= 8 && !pre ? 8 : 16; }
 int own_ctas(int sms, int D, int rows) {
   return sms * (D == 128 ? rows == 8 ? OwnCfg<128, 1>::kCtasPerSm : OwnCfg<128, 2>::kCtasPerSm
                          : OwnCfg<64, 1>::kCtasPerSm);
@@ -1376,7 +1479,8 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   };
   const size_t rows = static_cast<size_t>(n_seqs) * Hq;
   const int G = Hq / Hkv;
-  p->own_rows = own_unit_rows(G);
+  p->pre_in_own = prefixes_in_own(n_seqs, G, n_groups);
+  p->own_rows = own_unit_rows(G, p->pre_in_own);
   p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
   const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D, p->own_rows)) * p->own_rows;
   const size_t pre_rows = 4 * static_cast<size_t>(sms) * kPreTile;
@@ -1390,9 +1494,11 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
     p->own_row_o = reinterpret_cast<float*>(take(rows * D * 4));
     p->own_row_lse = reinterpret_cast<float*>(take(rows * 4));
     p->pre_meta = reinterpret_cast<int2*>(take(rows * 8));
-    p->pre_slot_o = reinterpret_cast<float*>(take(pre_rows * D * 4));
-    p->pre_slot_lse = reinterpret_cast<float*>(take(pre_rows * 4));
-    for (int ln = 0; ln < 2; ++ln) {
+    if (!p->pre_in_own) {
+      p->pre_slot_o = reinterpret_cast<float*>(take(pre_rows * D * 4));
+      p->pre_slot_lse = reinterpret_cast<float*>(take(pre_rows * 4));
+    }
+    for (int ln = 0; ln < (p->pre_in_own ? 1 : 2); ++ln) {
       p->pre_row_o[ln] = reinterpret_cast<float*>(take(rows * D * 4));
       p->pre_row_lse[ln] = reinterpret_cast<float*>(take(rows * 4));
     }
@@ -1410,14 +1516,18 @@ bool kv_map(CUtensorMap* map, const oomb_pool* pool, uint32_t rows, uint32_t bot
   return make_bf16_map(map, pool->kv, 4, dims, strides, box);
 }
 
+template <int D, int NT, bool PRE>
+bool own_attributes() {
+  return cudaFuncSetAttribute(own_kernel<D, NT, PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              OwnCfg<D, NT>::kSmem) == cudaSuccess;
+}
+
 template <int D>
 oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   if (!once_per_device(attr_done, [] {
-        return cudaFuncSetAttribute(own_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    OwnCfg<D, 1>::kSmem) == cudaSuccess &&
-               cudaFuncSetAttribute(own_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    OwnCfg<D, 2>::kSmem) == cudaSuccess &&
+        return own_attributes<D, 1, false>() && own_attributes<D, 2, false>() &&
+               own_attributes<D, 2, true>() &&
                cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     PreCfg<D>::kSmem) == cudaSuccess;
       }))
@@ -1430,7 +1540,8 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   cfg.attrs = attr;
   cudaError_t e = cudaSuccess;
   CUtensorMap map;
-  if (p.n_groups > 0) {
+  const bool prefix = p.n_groups > 0 && !p.pre_in_own;
+  if (prefix) {
     if (!kv_map(&map, pool, p.P, 1)) return OOMB_ERR_CUDA;
     cfg.gridDim = dim3(sms);
     cfg.blockDim = dim3(kPreThreads);
@@ -1442,14 +1553,11 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   if (e == cudaSuccess) {
     cfg.gridDim = dim3(own_ctas(sms, D, p.own_rows));
     cfg.blockDim = dim3(kOwnThreads);
-    cfg.numAttrs = p.n_groups > 0 ? 1 : 0;
-    if (p.own_rows == 8) {
-      cfg.dynamicSmemBytes = OwnCfg<D, 1>::kSmem;
-      e = cudaLaunchKernelEx(&cfg, own_kernel<D, 1>, p, map);
-    } else {
-      cfg.dynamicSmemBytes = OwnCfg<D, 2>::kSmem;
-      e = cudaLaunchKernelEx(&cfg, own_kernel<D, 2>, p, map);
-    }
+    cfg.numAttrs = prefix ? 1 : 0;
+    cfg.dynamicSmemBytes = p.own_rows == 8 ? OwnCfg<D, 1>::kSmem : OwnCfg<D, 2>::kSmem;
+    e = p.pre_in_own      ? cudaLaunchKernelEx(&cfg, own_kernel<D, 2, true>, p, map)
+        : p.own_rows == 8 ? cudaLaunchKernelEx(&cfg, own_kernel<D, 1, false>, p, map)
+                          : cudaLaunchKernelEx(&cfg, own_kernel<D, 2, false>, p, map);
   }
   if (e == cudaSuccess) {
     const int64_t rows = static_cast<int64_t>(p.n_seqs) * p.Hq;

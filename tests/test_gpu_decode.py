@@ -147,6 +147,35 @@ def test_many_sequences_behind_one_prefix(n, prefix):
         assert b.pg.status() == 0
 
 
+@pytest.mark.parametrize("heads", [(28, 4, 128, 64), (16, 2, 64, 16), (24, 1, 128, 16)])
+@pytest.mark.parametrize("rows,prefix", [(70, 300), (70, 700), (300, 200), (130, 129)])
+def test_many_groups_one_after_the_other(heads, rows, prefix):
+    """Many units of 128 or 256 rows for each thread block: what one leaves must not reach
+    the next.  The same bits every time, and the oracle's values."""
+    m = -(-rows * heads[1] // heads[0])
+    n = m * (1200 * 128 // max(rows, 128) // (4 * heads[1]))
+    starts = list(range(0, n, m))
+    with Batch(*heads, [0] * n, [*((s, prefix) for s in starts), (n, None)], seed=rows) as b:
+        o, lse = b.run()
+        b.check(o, lse, only=range(0, n, 41))
+        for _ in range(4):
+            o2, lse2 = b.run()
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        assert b.pg.status() == 0
+
+
+@pytest.mark.parametrize("heads", [(28, 4, 128, 64), (4, 2, 64, 16), (24, 1, 128, 16)])
+def test_groups_of_very_different_sizes(heads):
+    """One group of 60 sequences among 200 of one: few rows a group on average."""
+    rng = np.random.default_rng(17)
+    pre = [1000, *rng.integers(0, 60, 200).tolist()]
+    starts = [3, *range(63, 263)]
+    lens = rng.integers(0, 30, 270).tolist()
+    with Batch(*heads, lens, [*zip(starts, pre), (263, None)], seed=18) as b:
+        b.check(*b.run(), only=[0, 2, 3, 33, 62, *range(63, 270, 9), 262, 263, 269])
+        assert b.pg.status() == 0
+
+
 @pytest.mark.parametrize("n", [700, 2500])
 def test_many_short_sequences(n):
     rng = np.random.default_rng(n)
