@@ -1459,7 +1459,8 @@ bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_gr
 // rows, 2000 tokens 92 and 57 us.
 constexpr int kFewRows = 32;
 bool prefixes_in_own(int n_seqs, int G, int n_groups) {
-  return n_groups > 0 && static_cast<int64_t>(n_seqs) * G <= static_cast<int64_t>(kFewRows) * n_groups;
+  // (rounded down: a few sequences without a prefix do not count)
+  return n_groups > 0 && static_cast<int64_t>(n_seqs / n_groups) * G <= kFewRows;
 }
 // Rows of a unit of own_kernel: one column of 8, or two.
 int own_unit_rows(int G, bool pre) { return G <= 8 && !pre ? 8 : 16; }
