@@ -1297,13 +1297,14 @@ __device__ __forceinline__ int find_group(const DecodeParams& p, int b) {
 // W warps per row (sequence, head); a lane takes 4 values of a part, a warp
 // 128 / D parts at once.
 template <int D, int W>
-__global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const DecodeParams p) {
   constexpr int TPR = D / 4, PPW = 32 / TPR;
-  __shared__ float4 sx[4][TPR];
-  __shared__ float sm[4], sl[4];
+  constexpr int kWarps = W > 4 ? W : 4;
+  __shared__ float4 sx[kWarps][TPR];
+  __shared__ float sm[kWarps], sl[kWarps];
   const int warp = warp_id(), lane = lane_id();
   const long long n_rows = static_cast<long long>(p.n_seqs) * p.Hq;
-  const long long row = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
+  const long long row = static_cast<long long>(blockIdx.x) * (kWarps / W) + warp / W;
   const bool active = row < n_rows;
   const int b = active ? static_cast<int>(row / p.Hq) : 0, h = active ? static_cast<int>(row % p.Hq) : 0;
   int n_pre = 0, pre_row_in = 0;  // row of its 256-row unit
@@ -1426,8 +1427,19 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p) {
     }
     __syncthreads();
     if (w != 0) return;
+    top = -INFINITY;
 #pragma unroll
-    for (int v = 1; v < W; ++v) join(sm[warp + v], sl[warp + v], sx[warp + v][lane % TPR]);
+    for (int v = 0; v < W; ++v) top = fmaxf(top, sm[warp + v]);
+    total = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < W; ++v) {
+      const float t2 = sm[warp + v];
+      const float f = t2 == -INFINITY ? 0.f : fast_exp2(t2 - top);
+      const float4 y = sx[warp + v][lane % TPR];
+      total = fmaf(f, sl[warp + v], total);
+      x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+    }
   }
   if (!work || sub != 0) return;
   const float inv = total > 0.f ? 1.f / total : 0.f;
@@ -1452,15 +1464,19 @@ bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_gr
          static_cast<int64_t>(n_seqs) * Hq <= INT32_MAX;
 }
 
-// Prefix groups of few rows (sequences x query heads per KV head, on average) are units of
-// own_kernel: prefix_kernel takes 128 rows' time for them, and one more launch.  Both
-// ways, own_kernel first: 12 groups of 4 x 7 rows behind 1200 tokens (d = 128) 24.6 and
-// 28.7 us, behind 4000 54 and 51 us; 64 x 7 rows, 500 tokens 27 and 39 us; 30 x 35
-// rows, 2000 tokens 92 and 57 us.
-constexpr int kFewRows = 32;
-bool prefixes_in_own(int n_seqs, int G, int n_groups) {
-  // (rounded down: a few sequences without a prefix do not count)
-  return n_groups > 0 && static_cast<int64_t>(n_seqs / n_groups) * G <= kFewRows;
+// Prefix groups of few rows (sequences x query heads per KV head, on average; rounded
+// down: a few sequences without a prefix do not count) are units of own_kernel:
+// prefix_kernel takes 128 rows' time for them, and is one more launch.  own_kernel reads
+// the keys again for every 16 rows, which long prefixes pay for.  Both ways, own_kernel
+// first, d = 128, 4 KV heads: 64 groups of 7 rows behind 500 tokens 27 and 39 us; 6 x 14
+// rows, 16000 tokens 54 and 60; 12 x 28 rows, 1200 tokens (12 tiles per SM) 25 and 29;
+// 12 x 28 rows, 4000 tokens (41 per SM) 54 and 51; 30 x 35 rows, 2000 tokens 92 and 57.
+bool prefixes_in_own(int n_seqs, int G, int Hkv, int n_groups, int64_t max_len, int sms) {
+  if (n_groups == 0) return false;
+  const int64_t rows = static_cast<int64_t>(n_seqs / n_groups) * G;
+  if (rows <= 16) return true;
+  const int64_t tiles = 2ll * n_groups * Hkv * ((max_len + kOwnTile - 1) / kOwnTile);
+  return rows <= 32 && tiles <= 16ll * sms;
 }
 // Rows of a unit of own_kernel: one column of 8, or two.
 int own_unit_rows(int G, bool pre) { return G <= 8 && !pre ? 8 : 16; }
@@ -1470,8 +1486,8 @@ int own_ctas(int sms, int D, int rows) {
 }
 
 // Lays the workspace out from `base` (null: only counts) and returns its bytes.
-size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, int sms,
-               DecodeParams* p) {
+size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, bool pre_in_own,
+               int sms, DecodeParams* p) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* r = base ? base + at : nullptr;
@@ -1480,7 +1496,7 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   };
   const size_t rows = static_cast<size_t>(n_seqs) * Hq;
   const int G = Hq / Hkv;
-  p->pre_in_own = prefixes_in_own(n_seqs, G, n_groups);
+  p->pre_in_own = pre_in_own;
   p->own_rows = own_unit_rows(G, p->pre_in_own);
   p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
   const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D, p->own_rows)) * p->own_rows;
@@ -1505,6 +1521,16 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
     }
   }
   return at;
+}
+
+// Bytes of the workspace: enough for either way with the prefixes, which also goes by
+// lengths that are not known here.
+size_t workspace_bytes(int n_seqs, int Hq, int Hkv, int D, int n_groups, int sms) {
+  DecodeParams p;
+  size_t bytes = 0;
+  for (int own = 0; own < (n_groups > 0 ? 2 : 1); ++own)
+    bytes = std::max(bytes, lay_out(nullptr, n_seqs, Hq, Hkv, D, n_groups, own, sms, &p));
+  return bytes;
 }
 
 // K and V boxes of `rows` tokens x 64 columns x `both` (1: K or V, 2: K and V).
@@ -1562,13 +1588,15 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   }
   if (e == cudaSuccess) {
     const int64_t rows = static_cast<int64_t>(p.n_seqs) * p.Hq;
-    const bool wide = rows < 16 * static_cast<int64_t>(sms);
-    cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
-    cfg.blockDim = dim3(128);
+    // warps per row: as many as keep about every SM's warp slots filled once
+    const int w = rows < 4 * sms ? 16 : rows < 16 * sms ? 4 : 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(w == 1 ? (rows + 3) / 4 : rows));
+    cfg.blockDim = dim3(w == 16 ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    e = wide ? cudaLaunchKernelEx(&cfg, merge_kernel<D, 4>, p)
-             : cudaLaunchKernelEx(&cfg, merge_kernel<D, 1>, p);
+    e = w == 16  ? cudaLaunchKernelEx(&cfg, merge_kernel<D, 16>, p)
+        : w == 4 ? cudaLaunchKernelEx(&cfg, merge_kernel<D, 4>, p)
+                 : cudaLaunchKernelEx(&cfg, merge_kernel<D, 1>, p);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -1588,8 +1616,7 @@ extern "C" size_t oomb_decode_attn_workspace_size(int32_t n_seqs, int32_t num_q_
     cudaGetLastError();
     dev = 0;
   }
-  DecodeParams p;
-  return lay_out(nullptr, n_seqs, num_q_heads, num_kv_heads, head_dim, n_groups, sm_count(dev), &p);
+  return workspace_bytes(n_seqs, num_q_heads, num_kv_heads, head_dim, n_groups, sm_count(dev));
 }
 
 extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args* a, void* stream) {
@@ -1609,10 +1636,14 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
     return OOMB_ERR_INVALID_ARG;
   DecodeParams p;
   const int sms = sm_count(d.device);
+  const bool pre_in_own =
+      prefixes_in_own(a->n_seqs, Hq / d.num_kv_heads, d.num_kv_heads, a->n_groups,
+                      static_cast<int64_t>(a->max_prefix_pages) * d.page_size, sms);
   if (!a->workspace || !aligned16(a->workspace) ||
-      a->workspace_bytes < lay_out(static_cast<uint8_t*>(a->workspace), a->n_seqs, Hq,
-                                   d.num_kv_heads, D, a->n_groups, sms, &p))
+      a->workspace_bytes < workspace_bytes(a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups, sms))
     return OOMB_ERR_INVALID_ARG;
+  lay_out(static_cast<uint8_t*>(a->workspace), a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups,
+          pre_in_own, sms, &p);
   p.q = static_cast<const __nv_bfloat16*>(a->q);
   p.o = static_cast<__nv_bfloat16*>(a->o);
   p.lse = a->lse;
