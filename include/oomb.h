@@ -275,6 +275,7 @@ typedef struct oomb_rope_args {
   int32_t num_q_heads;
   int32_t rotary_dim;
   int32_t interleaved;        /* 0: pairs (i, i + rotary_dim / 2); 1: (2i, 2i + 1) */
+  int32_t num_kv_heads, head_dim, device; /* of the tensors: must be the pool's    */
 } oomb_rope_args;
 oomb_status oomb_kv_append_rope(oomb_pool* pool, const oomb_rope_args* args, void* stream);
 oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args, void* stream);
@@ -324,6 +325,7 @@ typedef struct oomb_decode_args {
   float softmax_scale;
   void* workspace;
   size_t workspace_bytes;
+  int32_t head_dim, device;    /* of the tensors: must be the pool's                */
 } oomb_decode_args;
 oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args* args, void* stream);
 /* Bytes of its workspace on the current device; 0 for arguments that it refuses. */

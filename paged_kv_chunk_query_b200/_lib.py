@@ -81,7 +81,9 @@ class RopeArgs(ctypes.Structure):
                 ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
                 ("n_tokens", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
-                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("device", ctypes.c_int32)]
 
 
 class DecodeArgs(ctypes.Structure):
@@ -93,7 +95,8 @@ class DecodeArgs(ctypes.Structure):
                 ("num_q_heads", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("n_groups", ctypes.c_int32), ("max_prefix_pages", ctypes.c_int32),
                 ("softmax_scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
-                ("workspace_bytes", ctypes.c_size_t)]
+                ("workspace_bytes", ctypes.c_size_t), ("head_dim", ctypes.c_int32),
+                ("device", ctypes.c_int32)]
 
 
 _lib = None
@@ -227,20 +230,20 @@ def _rows(t, shape, dev, name):
 
 
 def _stream_on(stream, dev):
-    """As _stream, but without one given the current stream of the tensors' device."""
+    """As _stream, but without one given the current stream of the tensors' device (its
+    raw handle: a torch.cuda.Stream takes longer to make than this library's call)."""
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _pool_on(pool, t, name):
-    """The pool's descriptor; `t` must be a tensor [rows][heads][head_dim] on its device."""
-    d = PoolDesc()
-    _check(load().oomb_pool_get_desc(pool, ctypes.byref(d)), "oomb_pool_get_desc")
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != d.device:
-        raise TypeError(f"{name} must be a tensor on the pool's device (cuda:{d.device})")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have the shape [rows][heads][head_dim], got "
-                         f"{tuple(t.shape)}")
-    return d
+def _heads_of(t, name):
+    """Device index and shape of a CUDA tensor [rows][heads][head_dim]; the library
+    compares them with the pool's."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have the shape [rows][heads][head_dim], got {tuple(shape)}")
+    return t.get_device(), shape
 
 
 # ------------------------------------------------------------------- pools
@@ -349,16 +352,15 @@ def kv_append(pool: int, page_ids: torch.Tensor, k: torch.Tensor, v: torch.Tenso
 # oomb_rope_args and oomb_decode_args as packed bytes (the layout of RopeArgs and
 # DecodeArgs, which a test holds them to): a tenth of the time that filling a
 # ctypes structure takes, for calls made once per token.
-_ROPE_PACK = struct.Struct("@9P4q6i")
-_DECODE_PACK = struct.Struct("@3P2q5P5ifPN")
+_ROPE_PACK = struct.Struct("@9P4q9i")
+_DECODE_PACK = struct.Struct("@3P2q5P5ifPN2i")
 
 
 def _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q, q_out,
                interleaved, names):
-    d = _pool_on(pool, k, names[0])
-    dev, n, n_seqs = d.device, k.shape[0], cached_lens.shape[0]
-    D = d.head_dim
-    shape = (n, d.num_kv_heads, D)
+    dev, shape = _heads_of(k, names[0])
+    n, H, D = shape
+    n_seqs = cached_lens.shape[0]
     kp, ks = _rows(k, shape, dev, names[0])
     vp, vs = _rows(v, shape, dev, names[1])
     qp = qs = op = os_ = hq = 0
@@ -376,7 +378,7 @@ def _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_f
         _arg(page_tables, i32, (n_seqs, max_pages), dev, "page_tables"),
         _arg(positions, i32, (n,), dev, "positions"),
         _arg(inv_freq, torch.float32, (half,), dev, "inv_freq"), kp, vp, qp, op, ks, vs, qs, os_,
-        n, n_seqs, max_pages, hq, 2 * half, bool(interleaved))
+        n, n_seqs, max_pages, hq, 2 * half, bool(interleaved), H, D, dev)
 
 
 def kv_append_rope(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_freq, q=None,
@@ -417,10 +419,8 @@ def decode_attn(pool, q, o, page_tables, seq_lens, softmax_scale, workspace, lse
     and, with prefix_pages [n_groups][max_prefix_pages], prefix_lens [n_groups] and
     group_start [n_groups + 1], over the prefix of the sequence's group, computed
     once for the group.  lse: optional fp32 [n_seqs][Hq] output."""
-    d = _pool_on(pool, q, "q")
-    dev, i32 = d.device, torch.int32
-    n, hq = q.shape[0], q.shape[1]
-    shape = (n, hq, d.head_dim)
+    dev, shape = _heads_of(q, "q")
+    (n, hq, D), i32 = shape, torch.int32
     qp, qs = _rows(q, shape, dev, "q")
     op, os_ = _rows(o, shape, dev, "o")
     lp = _arg(lse, torch.float32, (n, hq), dev, "lse") if lse is not None else 0
@@ -436,7 +436,7 @@ def decode_attn(pool, q, o, page_tables, seq_lens, softmax_scale, workspace, lse
     a = _DECODE_PACK.pack(
         qp, op, lp, qs, os_, _arg(page_tables, i32, (n, max_pages), dev, "page_tables"),
         _arg(seq_lens, i32, (n,), dev, "seq_lens"), pp, pl, gs, n, hq, max_pages, ng, mp,
-        softmax_scale, _arg(workspace, torch.uint8, (size,), dev, "workspace"), size)
+        softmax_scale, _arg(workspace, torch.uint8, (size,), dev, "workspace"), size, D, dev)
     _check(load().oomb_decode_attn(pool, a, _stream_on(stream, dev)), "oomb_decode_attn")
 
 

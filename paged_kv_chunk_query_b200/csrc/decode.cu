@@ -1623,6 +1623,7 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   if (!pool || !a || pool->desc.location != OOMB_LOC_DEVICE) return OOMB_ERR_INVALID_ARG;
   const oomb_pool_desc& d = pool->desc;
   const int D = d.head_dim, Hq = a->num_q_heads;
+  if (a->head_dim != D || a->device != d.device) return OOMB_ERR_INVALID_ARG;
   if (!good_shape(a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups)) return OOMB_ERR_INVALID_ARG;
   if (!(a->softmax_scale > 0.f)) return OOMB_ERR_INVALID_ARG;
   if (a->n_seqs == 0) return OOMB_OK;

@@ -359,6 +359,8 @@ bool good_rows(const void* p, int64_t stride, int64_t heads, int D) {
 oomb_status make_params(const oomb_pool* pool, const oomb_rope_args* a, bool bwd, RopeParams* p) {
   if (!pool || !a || pool->desc.location != OOMB_LOC_DEVICE) return OOMB_ERR_INVALID_ARG;
   const oomb_pool_desc& d = pool->desc;
+  if (a->num_kv_heads != d.num_kv_heads || a->head_dim != d.head_dim || a->device != d.device)
+    return OOMB_ERR_INVALID_ARG;
   if (a->n_tokens < 0 || a->n_seqs < 0) return OOMB_ERR_INVALID_ARG;
   if (bwd && !pool->grad) return OOMB_ERR_INVALID_ARG;
   if (a->rotary_dim < 0 || a->rotary_dim > d.head_dim || a->rotary_dim % 16)

@@ -339,7 +339,7 @@ def test_refusals_leave_everything_untouched():
                              lens.data_ptr(), kw["prefix_pages"].data_ptr(),
                              kw["prefix_lens"].data_ptr(), kw["group_start"].data_ptr(), 2, 4,
                              pages.shape[1], 1, kw["prefix_pages"].shape[1], 0.1, ws.data_ptr(),
-                             ws.numel())
+                             ws.numel(), 64, 0)
             for k, v in change.items():
                 setattr(a, k, v)
             return lib.oomb_decode_attn(b.pg.pool, ctypes.byref(a), None)
@@ -351,6 +351,7 @@ def test_refusals_leave_everything_untouched():
                        dict(num_q_heads=0), dict(n_seqs=-1), dict(n_seqs=65536),
                        dict(n_groups=3), dict(n_groups=-1), dict(softmax_scale=0.0),
                        dict(softmax_scale=float("nan")), dict(workspace=None),
+                       dict(head_dim=128), dict(device=1),
                        dict(workspace=ws.data_ptr() + 4), dict(workspace_bytes=ws.numel() - 1)):
             assert call(**change) == L.ERR_INVALID_ARG, change
         assert call(n_seqs=0, n_groups=0) == L.OK

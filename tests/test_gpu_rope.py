@@ -7,11 +7,14 @@ bf16 (half a step: 2^-8 of the value): |y - ref| <= 2^-8 |ref| + 2^-21 (|a| + |b
 Values and unrotated parts are copies: equal bits.  A page mean over r stored
 keys is a sum of r fp32 terms and a division: (r + 1) 2^-23 mean|k|.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_chunk_query_b200 as pk
+import paged_kv_chunk_query_b200._lib as L
 from oracle.rope import rotate
 from tests.ragged_harness import DEV, Pages, bf16, f64, i32, starts_of, tables
 
@@ -268,3 +271,56 @@ def test_captured_append_follows_new_lengths_on_another_stream():
             assert torch.equal(kv, pg.kv) and torch.equal(mean, pg.mean) and torch.equal(o, out)
             assert kv.any()
         del graph
+
+
+def test_refusals_leave_everything_untouched():
+    lib = L.load()
+    rng = np.random.default_rng(13)
+    k, v = (bf16(rng, 6, 2, 64).to(DEV) for _ in range(2))
+    q, out = bf16(rng, 6, 4, 64).to(DEV), torch.full((6, 4, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    f = torch.from_numpy(_freq(64)).to(DEV)
+    starts, cached, table, pos = i32([0, 6]), i32([0]), i32([[0]]), i32(list(range(6)))
+    with Pages(2, 16, 2, 64, True, fill=1.0) as pg, Pages(2, 16, 2, 64) as plain:
+        pg.grad.fill_(7.0)
+
+        def call(fn, pool=pg.pool, **change):
+            a = L.RopeArgs(starts.data_ptr(), cached.data_ptr(), table.data_ptr(), pos.data_ptr(),
+                           f.data_ptr(), k.data_ptr(), v.data_ptr(), q.data_ptr(), out.data_ptr(),
+                           128, 128, 256, 256, 6, 1, 1, 4, 64, 0, 2, 64, 0)
+            for name, value in change.items():
+                setattr(a, name, value)
+            return fn(pool, ctypes.byref(a), None)
+
+        for fn in (lib.oomb_kv_append_rope, lib.oomb_kv_append_rope_bwd):
+            for change in (dict(seq_start=None), dict(cached_lens=None), dict(page_tables=None),
+                           dict(positions=None), dict(inv_freq=None), dict(k=None), dict(v=None),
+                           dict(q=None), dict(q_out=None), dict(k_stride=120), dict(v_stride=64),
+                           dict(q_stride=252), dict(q_out_stride=8), dict(k=k.data_ptr() + 2),
+                           dict(n_tokens=-1), dict(n_seqs=-1), dict(max_pages=0),
+                           dict(num_q_heads=3), dict(num_q_heads=0), dict(interleaved=2),
+                           dict(num_kv_heads=1), dict(head_dim=128), dict(device=1),
+                           dict(q_out=q.data_ptr(), q_out_stride=512)):
+                assert call(fn, **change) == L.ERR_INVALID_ARG, change
+            for rot in (-16, 8, 24, 80):
+                assert call(fn, rotary_dim=rot) == L.ERR_UNSUPPORTED
+            assert call(fn, n_tokens=0) == L.OK and call(fn, n_seqs=0) == L.OK
+        assert call(lib.oomb_kv_append_rope_bwd, pool=plain.pool) == L.ERR_INVALID_ARG
+        torch.cuda.synchronize()
+        assert (pg.kv == 1.0).all() and (pg.grad == 7.0).all() and (out == 3.0).all()
+        assert pg.status() == 0
+        args = (starts, cached, table, pos, f)
+        with pytest.raises(pk.OombError):  # one KV head where the pool has two
+            pk.kv_append_rope(pg.pool, k[:, :1].contiguous(), v[:, :1].contiguous(), *args)
+        with pytest.raises(ValueError):
+            pk.kv_append_rope(pg.pool, k, v[:5], *args)
+        with pytest.raises(ValueError):
+            pk.kv_append_rope(pg.pool, k[..., :32], v[..., :32], *args)
+        with pytest.raises(ValueError):
+            pk.kv_append_rope(pg.pool, k, v, *args, q=q)
+        with pytest.raises(ValueError):
+            pk.kv_append_rope(pg.pool, k, v, i32([0, 3, 6]), *args[1:])
+        with pytest.raises(TypeError):
+            pk.kv_append_rope(pg.pool, k.float(), v, *args)
+        with pytest.raises(TypeError):
+            pk.kv_append_rope(pg.pool, k, v, starts.long(), *args[1:])
+        assert (pg.kv == 1.0).all()
