@@ -19,6 +19,7 @@ namespace {
 using namespace oomb;
 
 constexpr int kThreads = 256;
+constexpr int kMeanThreads = 512;
 constexpr int kMaxTile = 32; // tokens per CTA
 constexpr int kMaxHalf = 64; // pairs of a head
 
@@ -72,7 +73,7 @@ __device__ __forceinline__ void count_starts(const RopeParams& p, int t0, int n,
   for (int i = t, s = first; i <= p.n_seqs;) {
     if (s <= t0) ++before;
     else if (s < t0 + n) atomicAdd(&mark[s - t0], 1);
-    if ((i += kThreads) <= p.n_seqs) s = p.seq_start[i];
+    if ((i += blockDim.x) <= p.n_seqs) s = p.seq_start[i];
   }
   before = __reduce_add_sync(0xffffffffu, before);
   if (before && t % 32 == 0) atomicAdd(&mark[0], before);
@@ -289,41 +290,53 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
 }
 
 // Representatives of the pages that received tokens: the mean of the stored
-// keys of rows [0, r], r the last row written.  One warp per (page, head), the
-// one that finds the page's last new token in its CTA's tile.  Keys are summed
-// anew rather than added to the old mean: a sequence that was cut back to
-// fewer tokens and went on gets the right mean, and the call can be repeated.
+// keys of rows [0, r], r the last row written; the CTA that finds a page's last new
+// token in its tile takes it.  Keys are summed anew rather than added to the old mean:
+// a sequence that was cut back to fewer tokens and went on gets the right mean, and
+// the call can be repeated.  One warp per (page, head), or up to 16 where a CTA has
+// few of them: the load latency of 64 rows is then paid once.
 template <int D>
-__global__ void __launch_bounds__(kThreads) page_mean_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kMeanThreads, 2) page_mean_kernel(const RopeParams p) {
   constexpr int VPR = D / 8;      // 16-byte vectors per row
   constexpr int RPW = 32 / VPR;   // rows that a warp reads at once
-  constexpr int kBatch = 16;      // loads in flight per lane
+  constexpr int kWarps = kMeanThreads / 32;
+  constexpr int kBatch = 8;       // loads in flight per lane
   __shared__ Places pl;
-  __shared__ int mark[32];
+  __shared__ int mark[32], tok[32], n_pages;
+  __shared__ __align__(16) float red[kWarps][D];
   const int t0 = blockIdx.x * p.tile;
   const int n = min(p.tile, p.n_tokens - t0);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   count_starts(p, t0, n, threadIdx.x <= p.n_seqs ? p.seq_start[threadIdx.x] : 0, mark);
-  if (threadIdx.x < 32) find_places(p, t0, n, &pl, mark, false);
+  if (warp == 0) {
+    find_places(p, t0, n, &pl, mark, false);
+    const bool last = pl.last[lane] && pl.page[lane] >= 0;
+    const unsigned all = __ballot_sync(0xffffffffu, last);
+    if (last) tok[__popc(all & ((1u << lane) - 1))] = lane;
+    if (lane == 0) n_pages = __popc(all);
+  }
   __syncthreads();
   pdl_wait();  // the keys of this call are in the pages
-  const int lane = threadIdx.x % 32, vec = lane % VPR, sub = lane / VPR;
-  for (int i = threadIdx.x / 32; i < n * p.Hkv; i += kThreads / 32) {
-    const int j = i / p.Hkv, g = i % p.Hkv;
-    if (!pl.last[j] || pl.page[j] < 0) continue;
+  const int items = n_pages * p.Hkv;
+  int share = 1;  // warps per (page, head)
+  while (2 * share <= kWarps && 2 * share * items <= kWarps) share *= 2;
+  const int vec = lane % VPR, sub = lane / VPR, part = warp % share;
+  for (int i = warp / share; i < items; i += kWarps / share) {
+    const int j = tok[i / p.Hkv], g = i % p.Hkv;
     const size_t head = static_cast<size_t>(pl.page[j]) * p.Hkv + g;
     const __nv_bfloat16* src = p.kv + head * 2 * p.P * D + vec * 8;
-    const int rows = pl.row[j] + 1;
+    const int rows = pl.row[j] + 1, step = share * RPW;
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int r0 = sub; r0 < rows; r0 += kBatch * RPW) {
+    for (int r0 = part * RPW + sub; r0 < rows; r0 += kBatch * step) {
       uint4 v[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b)
-        if (r0 + b * RPW < rows) v[b] = *reinterpret_cast<const uint4*>(src + (r0 + b * RPW) * D);
+        if (r0 + b * step < rows) v[b] = *reinterpret_cast<const uint4*>(src + (r0 + b * step) * D);
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        if (r0 + b * RPW >= rows) break;
+        if (r0 + b * step >= rows) break;
         float x[8];
         unpack8(v[b], x);
 #pragma unroll
@@ -332,15 +345,29 @@ __global__ void __launch_bounds__(kThreads) page_mean_kernel(const RopeParams p)
     }
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 8; ++e)
 #pragma unroll
       for (int m = VPR; m < 32; m *= 2) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], m);
-      acc[e] /= static_cast<float>(rows);
+    if (share > 1) {  // one round: the (page, head)s are no more than the warps
+      if (sub == 0) {
+        float4* mine = reinterpret_cast<float4*>(red[warp] + vec * 8);
+        mine[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        mine[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / share), "r"(32 * share) : "memory");
+      if (part != 0) continue;
+      for (int w = 1; w < share; ++w) {
+        const float4* other = reinterpret_cast<const float4*>(red[warp + w] + vec * 8);
+        const float4 a = other[0], b = other[1];
+        acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+        acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
+      }
     }
     if (sub == 0) {
+      const float k = static_cast<float>(rows);
       float4* dst = reinterpret_cast<float4*>(p.summary + head * D + vec * 8);
-      dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      dst[0] = make_float4(acc[0] / k, acc[1] / k, acc[2] / k, acc[3] / k);
+      dst[1] = make_float4(acc[4] / k, acc[5] / k, acc[6] / k, acc[7] / k);
     }
   }
 }
@@ -439,10 +466,11 @@ extern "C" oomb_status oomb_kv_append_rope(oomb_pool* pool, const oomb_rope_args
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   launch_rope<false>(p, d.head_dim, s);
   // page means: a dependent launch, its search for the pages runs beside the rotation
-  p.tile = std::min(32, std::max(1, p.n_tokens / sm_count(d.device)));
+  const int slots = 2 * sm_count(d.device);
+  p.tile = std::min(32, (p.n_tokens + slots - 1) / slots);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((p.n_tokens + p.tile - 1) / p.tile);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kMeanThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
