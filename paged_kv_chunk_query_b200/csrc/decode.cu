@@ -112,54 +112,81 @@ __device__ __forceinline__ long long fast_div(long long a, long long b) {
   return a / b;
 }
 
-// The CTA's range [t0, t1) of a row of `total` tiles cut into equal parts, and
-// the item (of n items with weight(i) tiles each) in which t0 lies: all threads
-// sum weights of n / blockDim consecutive items each.
+// The CTA's range [t0, t1) of a row of `total` places cut into equal parts, and the
+// item (of n) in which t0 lies.  weight(i) gives an item's key tiles and units; each
+// unit takes `cost` places more than its tiles, for what its start and end take: as
+// many as a CTA has tiles, less one, but at most COST.  All threads sum the weights of
+// n / blockDim consecutive items each.
+struct Weight {
+  long long tiles, units;
+};
 struct Range {
   long long total, per, t0, t1;
-  long long item_at;  // first tile of the item
-  int item;
+  long long item_at;  // first place of the item
+  int item, cost;
 };
-template <int NT, class W>
+template <int NT, int COST, class W>
 __device__ __forceinline__ Range find_range(int n, W weight) {
-  __shared__ long long warp_sum[NT / 32];
+  __shared__ Weight warp_sum[NT / 32];
   __shared__ Range sh;
   const int t = threadIdx.x;
   const int each = (n + NT - 1) / NT, i0 = min(n, t * each), i1 = min(n, i0 + each);
-  long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += weight(i, true);
-  long long inc = mine;
+  Weight mine{0, 0};
+  for (int i = i0; i < i1; ++i) {
+    const Weight w = weight(i, true);
+    mine.tiles += w.tiles;
+    mine.units += w.units;
+  }
+  Weight inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, d);
-    if ((t & 31) >= d) inc += v;
+    const long long a = __shfl_up_sync(0xffffffffu, inc.tiles, d);
+    const long long b = COST ? __shfl_up_sync(0xffffffffu, inc.units, d) : 0;
+    if ((t & 31) >= d) {
+      inc.tiles += a;
+      inc.units += b;
+    }
   }
   if ((t & 31) == 31) warp_sum[t / 32] = inc;
   __syncthreads();
-  long long before = inc - mine, total = 0;
+  Weight before{inc.tiles - mine.tiles, inc.units - mine.units}, all{0, 0};
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    if (w < t / 32) before += warp_sum[w];
-    total += warp_sum[w];
+    const Weight x = warp_sum[w];
+    if (w < t / 32) {
+      before.tiles += x.tiles;
+      before.units += x.units;
+    }
+    all.tiles += x.tiles;
+    all.units += x.units;
   }
-  const long long per = fast_div(total + gridDim.x - 1, gridDim.x);
-  const long long t0 = min(total, per * blockIdx.x), t1 = min(total, t0 + per);
-  if (t0 < t1 && before <= t0 && t0 < before + mine) {
+  Range r;
+  r.cost = 0;
+  r.total = all.tiles;
+  r.per = fast_div(r.total + gridDim.x - 1, gridDim.x);
+  if (COST) {
+    r.cost = static_cast<int>(min(max(r.per - 1, 0ll), static_cast<long long>(COST)));
+    r.total += r.cost * all.units;
+    r.per = fast_div(r.total + gridDim.x - 1, gridDim.x);
+  }
+  r.t0 = min(r.total, r.per * blockIdx.x);
+  r.t1 = min(r.total, r.t0 + r.per);
+  long long at = before.tiles + r.cost * before.units;
+  const long long end = at + mine.tiles + r.cost * mine.units;
+  if (r.t0 < r.t1 && at <= r.t0 && r.t0 < end) {
     int i = i0;
     for (;; ++i) {
-      const long long w = weight(i, false);
-      if (t0 < before + w) break;
-      before += w;
+      const Weight w = weight(i, false);
+      const long long places = w.tiles + r.cost * w.units;
+      if (r.t0 < at + places) break;
+      at += places;
     }
     sh.item = i;
-    sh.item_at = before;
+    sh.item_at = at;
   }
   __syncthreads();
-  Range r = sh;
-  r.total = total;
-  r.per = per;
-  r.t0 = t0;
-  r.t1 = t1;
+  r.item = sh.item;
+  r.item_at = sh.item_at;
   return r;
 }
 
@@ -312,10 +339,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
     *reinterpret_cast<uint4*>(sq + i) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
   const int n_items = (PRE ? p.n_groups : 0) + p.n_seqs;
-  const Range rg = find_range<kOwnThreads>(n_items, [&](int i, bool note) {
+  const Range rg = find_range<kOwnThreads, 0>(n_items, [&](int i, bool note) {
     Item it;
     it.load(p, i, note && blockIdx.x == 0 ? p.status : nullptr);
-    return it.weight(p);
+    return Weight{it.weight(p), 0};
   });
   const int n_mine = static_cast<int>(rg.t1 - rg.t0);
 
@@ -727,51 +754,81 @@ constexpr int kPreThreads = 384;
 // Steps through the CTA's share.  A unit is one KV head and up to 256 rows of a
 // group, 128 for each of the two softmax lanes; both take the same key tile in a
 // step.  Where only 128 rows are left, both lanes have these rows and take two key
-// tiles a step (`split`), lane 1 every second one.
+// tiles a step (`split`), lane 1 every second one.  A unit takes `cost` places behind
+// its steps in the row that is cut among the CTAs: a CTA with the end of one unit and the
+// start of the next, which take as long as four steps, gets fewer steps (d = 128: 96
+// sequences behind 8191 tokens 46.2 -> 43.5 us, 37 behind 32768 55.7 -> 50.3; for d = 64,
+// where less is written at the end, the longer ranges cost as much as they save: 256
+// behind 8192 tokens 35.4 us without, 37.1 with).
+template <int D>
+constexpr int kUnitCost = D == 128 ? 4 : 0;
 struct PreWalk {
   Group gr;
   int j, g, pair, step;
   int nt, row_tiles;
+  int cost, left;  // places of a unit's end; places left of the CTA's range
+  int here;        // steps of the current unit in this CTA
   __device__ __forceinline__ void load(const DecodeParams& p, uint32_t* status = nullptr) {
     gr = group_of(p, j, status);
     nt = (gr.len + kPreTile - 1) / kPreTile;
     row_tiles = static_cast<int>(
         (static_cast<long long>(gr.hi - gr.lo) * p.G + kPreTile - 1) / kPreTile);
   }
-  // steps of one KV head, and of the group
-  __device__ __forceinline__ long long head_steps() const {
-    return static_cast<long long>(row_tiles / 2) * nt + (row_tiles & 1) * ((nt + 1) / 2);
-  }
-  __device__ __forceinline__ long long weight(const DecodeParams& p) const {
-    return head_steps() * p.Hkv;
+  __device__ __forceinline__ bool none() const { return nt == 0 || row_tiles == 0; }
+  // steps and units of one KV head
+  __device__ __forceinline__ Weight head() const {
+    if (none()) return Weight{0, 0};
+    return Weight{static_cast<long long>(row_tiles / 2) * nt + (row_tiles & 1) * ((nt + 1) / 2),
+                  (row_tiles + 1) / 2};
   }
   __device__ __forceinline__ bool split() const { return 2 * pair + 1 == row_tiles; }
   __device__ __forceinline__ int steps() const { return split() ? (nt + 1) / 2 : nt; }
-  // key tile of a lane in this step; it has none where this is not below nt
-  __device__ __forceinline__ int tile(int ln) const { return split() ? 2 * step + ln : step; }
+  __device__ __forceinline__ bool ends() const { return step + here == steps(); }
+  // key tile of a lane i steps on; it has none where this is not below nt
+  __device__ __forceinline__ int tile(int i, int ln) const {
+    return split() ? 2 * (step + i) + ln : step + i;
+  }
+  // CTAs with steps of this unit, which begins here
+  __device__ __forceinline__ int parts(int per) const {
+    const int over = steps() - left;
+    return over <= 0 ? 1 : 1 + (over + per - 1) / per;
+  }
   __device__ __forceinline__ void start(const DecodeParams& p, const Range& r) {
     j = r.item;
     load(p);
-    const long long off = r.t0 - r.item_at, hs = head_steps();
-    g = static_cast<int>(fast_div(off, hs));
-    const long long rem = off - g * hs;
-    pair = static_cast<int>(min(fast_div(rem, nt), static_cast<long long>(row_tiles / 2)));
-    step = static_cast<int>(rem - static_cast<long long>(pair) * nt);
+    cost = r.cost;
+    left = static_cast<int>(r.t1 - r.t0);
+    here = 0;
+    const Weight h = head();
+    const long long off = r.t0 - r.item_at, hp = h.tiles + cost * h.units;
+    g = static_cast<int>(fast_div(off, hp));
+    const long long rem = off - g * hp;
+    pair = static_cast<int>(min(fast_div(rem, nt + cost), h.units - 1));
+    step = static_cast<int>(rem - static_cast<long long>(pair) * (nt + cost));
   }
-  // n steps on, within the unit or to the start of the next one
-  __device__ __forceinline__ void skip(const DecodeParams& p, int n, bool more) {
-    step += n;
-    if (step < steps()) return;
-    step = 0;
-    if (++pair < (row_tiles + 1) / 2) return;
-    pair = 0;
-    if (++g < p.Hkv) return;
-    g = 0;
-    if (!more) return;
-    do {
-      ++j;
-      load(p);
-    } while (weight(p) == 0);
+  // On to the next unit with steps of this CTA, if there is one.
+  __device__ __forceinline__ bool next(const DecodeParams& p) {
+    step += here;
+    left -= here;
+    here = 0;
+    while (left > 0) {
+      if (step < steps()) {
+        here = min(steps() - step, left);
+        return true;
+      }
+      left -= steps() + cost - step;
+      step = 0;
+      if (++pair < (row_tiles + 1) / 2) continue;
+      pair = 0;
+      if (++g < p.Hkv) continue;
+      g = 0;
+      if (left <= 0) break;
+      do {
+        ++j;
+        load(p);
+      } while (none());
+    }
+    return false;
   }
 };
 
@@ -873,14 +930,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     mbar_init(&bar_drain, 1);
     fence_mbar_init();
   }
-  const Range rg = find_range<kPreThreads>(p.n_groups, [&](int j, bool note) {
+  const Range rg = find_range<kPreThreads, kUnitCost<D>>(p.n_groups, [&](int j, bool note) {
     PreWalk w;
     w.j = j;
     w.load(p, note && blockIdx.x == 0 ? p.status : nullptr);
-    return w.weight(p);
+    const Weight h = w.head();
+    return Weight{h.tiles * p.Hkv, h.units * p.Hkv};
   });
   if (rg.t0 >= rg.t1) return;  // the same for all threads of the CTA
-  const int n_mine = static_cast<int>(rg.t1 - rg.t0), per = static_cast<int>(rg.per);
+  const int per = static_cast<int>(rg.per);
   if (warp == 8) {
     tmem_alloc(&tmem_base_sh, Cfg::kTmemCols);
     tmem_relinquish();
@@ -931,11 +989,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                       &full[st], hf * 64, 0, 2 * w.g + which, page);
         return true;
       };
-      for (int i = 0; ok && i < n_mine; ++i) {
-        const int ta = w.tile(0), tb = w.tile(1);
-        const bool two = w.split() && tb < w.nt;
-        ok = load(ta, 0) && (!two || load(tb, 0)) && load(ta, 1) && (!two || load(tb, 1));
-        w.skip(p, 1, i + 1 < n_mine);
+      while (ok && w.next(p)) {
+        for (int i = 0; ok && i < w.here; ++i) {
+          const int ta = w.tile(i, 0), tb = w.tile(i, 1);
+          const bool two = w.split() && tb < w.nt;
+          ok = load(ta, 0) && (!two || load(tb, 0)) && load(ta, 1) && (!two || load(tb, 1));
+        }
       }
       if (lane == 0) {
         issued_sh = issued;
@@ -998,13 +1057,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           __syncwarp();
         }
       };
-      for (int left = n_mine; ok && left > 0;) {
+      while (ok && __shfl_sync(0xffffffffu, w.next(p), 0)) {
         // a unit: its steps here, whether lane 1 has a tile of its own, and in the last step
-        const int here = __shfl_sync(0xffffffffu, min(left, w.steps() - w.step), 0);
+        const int here = __shfl_sync(0xffffffffu, w.here, 0);
         const bool split = __shfl_sync(0xffffffffu, w.split(), 0);
-        const bool odd = __shfl_sync(
-            0xffffffffu, w.split() && w.step + here == w.steps() && (w.nt & 1), 0);
-        left -= here;
+        const bool odd = __shfl_sync(0xffffffffu, w.split() && w.ends() && (w.nt & 1), 0);
         // the lanes' queries come when the old unit's O has been read
         const bool two0 = !(odd && here == 1);
         for (int ln = 0; ln < 1 + two0; ++ln) {
@@ -1039,7 +1096,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             if (ntwo) qk(1, pos.at(1), false, true);
           }
         }
-        w.skip(p, here, left > 0);
       }
       if (!ok) {
         *abort_flag = 1;
@@ -1062,13 +1118,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     size_t out_row = 0;
     int cnt = 0, n_s = 0, n_units = 0;
     bool ok = true, valid = false, begins = false, any = false;
-    for (int i = 0; ok && i < n_mine; ++i) {
+    while (ok && w.next(p)) for (int i = 0; ok && i < w.here; ++i) {
       const bool split = w.split();
-      const bool two = !split || w.tile(1) < w.nt, extra = split && two;
+      const bool two = !split || w.tile(i, 1) < w.nt, extra = split && two;
       const int vc = cnt + 1 + extra + (extra ? ln : 0);  // ring index of this lane's V tile
       cnt += 2 + 2 * extra;
       const bool mine = ln == 0 || two;
-      if (i == 0 || w.step == 0) {
+      if (i == 0) {
         // this thread's row of the unit
         const unsigned rr = (2u * w.pair + (split ? 0 : ln)) * kPreTile + r;
         const unsigned rs = rr / static_cast<unsigned>(p.G);
@@ -1095,16 +1151,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (lane == 0) mbar_arrive(&bar_q[ln]);
         }
         if (valid && begins && (ln == 0 || !split)) {
-          const int over = w.steps() - (n_mine - i);  // steps in later CTAs
-          const int n = over <= 0 ? 1 : 1 + (over + per - 1) / per;
-          p.pre_meta[out_row] = make_int2(blockIdx.x, 2 * n + split);
+          p.pre_meta[out_row] = make_int2(blockIdx.x, 2 * w.parts(per) + split);
         }
         m_used = -INFINITY;
         l = 0.f;
         any = false;
       }
       if (mine) {
-        const int tile = w.tile(ln);
+        const int tile = w.tile(i, ln);
         // a listed page that is none: its keys are masked (its tile holds zeros)
         bool bad_page = false;
         {
@@ -1204,9 +1258,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         l = l * alpha + (la + lb);
       }
 
-      if (i == n_mine - 1 || w.step == w.steps() - 1) {
+      if (i == w.here - 1) {
         // ------------------------------------------------ end of a unit
-        const bool whole = begins && w.step == w.steps() - 1;
+        const bool whole = begins && w.ends();
         const size_t slot_row =
             ((static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * 2 + ln) * kPreTile + r;
         float* od = whole ? p.pre_row_o[split ? ln : 0] + out_row * D : p.pre_slot_o + slot_row * D;
@@ -1254,7 +1308,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               any && l > 0.f ? m_used + log2f(l) : -INFINITY;
         tc_fence_before();  // these reads come before the next unit's products
       }
-      w.skip(p, 1, i + 1 < n_mine);
     }
     if (!ok) {
       *abort_flag = 1;
