@@ -7,10 +7,10 @@
 //   LSE = ln sum e^LSE_k,  O = sum e^(LSE_k - LSE) O_k.
 //
 // Three kernels, each a dependent launch of the one before:
-//   prefix_kernel (with prefix groups)  256 rows (sequence, head) of a group at
-//       once against the prefix's keys: its K and V are read once per 256 rows
-//       instead of once per sequence.  tcgen05, bound by the tensor cores and
-//       the exponentials for many rows, by memory for few.
+//   prefix_kernel (with prefix groups of more than a few rows)  256 rows (sequence,
+//       head) of a group at once against the prefix's keys: its K and V are read once
+//       per 256 rows instead of once per sequence.  tcgen05, bound by the tensor cores
+//       for many rows, by memory for few.
 //   own_kernel   8 or 16 query heads of one KV head of one sequence against its
 //       own keys.  Each K and V value is used for these few rows only: bound by
 //       memory, its matrix products are small (mma.sync m16n8k16).
@@ -100,9 +100,10 @@ __device__ __forceinline__ Group group_of(const DecodeParams& p, int j, uint32_t
   return r;
 }
 
-// Tiles of sequence b in own_kernel, all its units; an empty sequence has one
-// (all masked) per unit, which writes its result.
-__device__ __forceinline__ int own_tiles(int len) { return max(1, (len + kOwnTile - 1) / kOwnTile); }
+// Tiles of a length; an empty sequence of own_kernel has one (all masked) per unit,
+// which writes its result.
+__device__ __forceinline__ int tiles_of(int len, int tile) { return len > 0 ? (len - 1) / tile + 1 : 0; }
+__device__ __forceinline__ int own_tiles(int len) { return max(1, tiles_of(len, kOwnTile)); }
 
 // Quotients of 64-bit numbers that nearly always fit 32 bits, where a division
 // takes a fifth of the time.
@@ -282,7 +283,7 @@ struct OwnItem {
       len = checked_len(raw_len, p.max_prefix_pages, p.P, status);
       table = p.prefix_pages + static_cast<size_t>(i) * p.max_prefix_pages;
       rows = (hi - lo) * p.G;
-      nt = (len + kOwnTile - 1) / kOwnTile;
+      nt = tiles_of(len, kOwnTile);
       row_tiles = (rows + ROWS - 1) / ROWS;
     } else {
       lo = PRE ? i - p.n_groups : i;
@@ -770,7 +771,7 @@ struct PreWalk {
   int here;        // steps of the current unit in this CTA
   __device__ __forceinline__ void load(const DecodeParams& p, uint32_t* status = nullptr) {
     gr = group_of(p, j, status);
-    nt = (gr.len + kPreTile - 1) / kPreTile;
+    nt = tiles_of(gr.len, kPreTile);
     row_tiles = static_cast<int>(
         (static_cast<long long>(gr.hi - gr.lo) * p.G + kPreTile - 1) / kPreTile);
   }
@@ -1005,7 +1006,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       // The whole warp goes through this code with the same values in every lane (those
       // that come from memory are made so by a shuffle): the descriptors then live in
       // uniform registers.  Issued from a branch of one lane, each product first moves
-      // its operands there, and takes twice the tensor core's time.
+      // its operands there, and takes longer than the tensor core needs for it (256
+      // sequences behind 32773 tokens: 213 us so, 153 us in this form).
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
       // low words of the descriptors (address / 16, leading offset); the high words are constant

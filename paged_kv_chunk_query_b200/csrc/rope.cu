@@ -200,18 +200,19 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
   const int eb = !IL && turned ? ea + p.half : ea + 8;
   const int kv_heads = 2 * p.Hkv, heads = kv_heads + p.Hq;
   const int h_mine = warp % wpt * HPP + lane / UPH, h_step = wpt * HPP;
-  const int h_from = (BWD ? kv_heads : 0) + h_mine;  // backward: queries first
+  const int h_from = h_mine, h_to = BWD ? p.Hq : heads;  // backward: queries first
   uint4 xa[kBatch], xb[kBatch];
   auto load = [&](int j, int h0) {
     const size_t tok = t0 + j;
-    const __nv_bfloat16* qrow = p.q + tok * p.q_stride - kv_heads * D;
+    const __nv_bfloat16* qrow = p.q + tok * p.q_stride - (BWD ? 0 : kv_heads * D);
     const __nv_bfloat16* krow = p.k + tok * p.k_stride;
     const __nv_bfloat16* vrow = p.v + tok * p.v_stride - p.Hkv * D;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = h0 + i * h_step;
-      if (h < heads) {
-        const __nv_bfloat16* src = (h >= kv_heads ? qrow : h >= p.Hkv ? vrow : krow) + h * D;
+      if (h < h_to) {
+        const __nv_bfloat16* src =
+            (BWD || h >= kv_heads ? qrow : h >= p.Hkv ? vrow : krow) + h * D;
         xa[i] = *reinterpret_cast<const uint4*>(src + ea);
         xb[i] = *reinterpret_cast<const uint4*>(src + eb);
       }
@@ -229,22 +230,22 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
   const size_t head_elems = static_cast<size_t>(p.P) * D;
   for (int j = j_from; j < n; j += j_step) {
     const size_t tok = t0 + j;
-    const int page = pl.page[j];
+    const int page = BWD ? 0 : pl.page[j];  // the backward needs it later, and registers now
     const bool used = pl.used[j];
     const float* cj = cs + j * p.half + 8 * u;
     const float* sj = sn + j * p.half + 8 * u;
     // the token's row of KV head 0's keys in the pool
-    const size_t pool_row = page < 0 ? 0
-                                     : static_cast<size_t>(page) * kv_heads * head_elems +
-                                           static_cast<size_t>(pl.row[j]) * D;
-    __nv_bfloat16* orow = p.q_out + tok * p.q_out_stride - kv_heads * D;
-    for (int h0 = h_from; h0 < heads; h0 += kBatch * h_step) {
+    const size_t pool_row = BWD || page < 0 ? 0
+                                            : static_cast<size_t>(page) * kv_heads * head_elems +
+                                                  static_cast<size_t>(pl.row[j]) * D;
+    __nv_bfloat16* orow = p.q_out + tok * p.q_out_stride - (BWD ? 0 : kv_heads * D);
+    for (int h0 = h_from; h0 < h_to; h0 += kBatch * h_step) {
       if (j != j_from || h0 != h_from) load(j, h0);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = h0 + i * h_step;
-        if (h >= heads) break;
-        const bool is_q = h >= kv_heads, is_v = !is_q && h >= p.Hkv;
+        if (h >= h_to) break;
+        const bool is_q = BWD || h >= kv_heads, is_v = !is_q && h >= p.Hkv;
         if (is_q ? !used : page < 0) continue;
         // blocks of a page: K and V of KV head 0, of KV head 1, ...
         const int block = is_v ? 2 * (h - p.Hkv) + 1 : 2 * h;
@@ -267,12 +268,14 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
         }
       }
     }
-    if (BWD && page >= 0) {
+    if (BWD && pl.page[j] >= 0) {
       // the fp32 gradients of the token's keys and values
+      const float* grad_row = p.grad + static_cast<size_t>(pl.page[j]) * kv_heads * head_elems +
+                              static_cast<size_t>(pl.row[j]) * D;
 #pragma unroll 2
       for (int h = h_mine; h < kv_heads; h += h_step) {
         const bool is_v = h >= p.Hkv;
-        const float* src = p.grad + pool_row + (is_v ? 2 * (h - p.Hkv) + 1 : 2 * h) * head_elems;
+        const float* src = grad_row + (is_v ? 2 * (h - p.Hkv) + 1 : 2 * h) * head_elems;
         float x[8], y[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
