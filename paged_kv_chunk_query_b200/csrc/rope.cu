@@ -22,6 +22,7 @@ constexpr int kThreads = 256;
 constexpr int kMeanThreads = 512;
 constexpr int kMaxTile = 32; // tokens per CTA
 constexpr int kMaxHalf = 64; // pairs of a head
+constexpr int kBatch = 3;    // rounds of loads that a warp has under way
 
 struct RopeParams {
   const int32_t* seq_start;
@@ -43,6 +44,7 @@ struct RopeParams {
   int interleaved;
   int lg_p;         // log2(P)
   int tile;         // tokens per CTA
+  int batch;        // rounds of heads per piece, at most kBatch
 };
 
 __device__ __forceinline__ void pdl_launch_dependents() {
@@ -174,17 +176,16 @@ __device__ __forceinline__ void rotate(float* x, float* y, const float* cs, cons
   }
 }
 
-// One CTA: `tile` <= 32 tokens; 8 / tile warps for each, or each warp a token after
-// the other.  A warp takes the token's heads (counted K, V, then Q) 32 / (D / 16)
-// at a time.  A lane has the same two 16-byte vectors of each head, values [ea,
-// ea + 8) and [eb, eb + 8), chosen so that eight pairs lie in them; nothing is
-// divided per head.  The loads of a warp's first kBatch rounds are issued before
-// the angles and places are known.
+// One CTA: `tile` <= 32 tokens.  A warp takes heads of a token (counted K, V, then Q)
+// 32 / (D / 16) at a time, `batch` <= kBatch times; these pieces of all the CTA's
+// tokens are dealt out to its warps in turn.  A lane has the same two 16-byte vectors
+// of each head, values [ea, ea + 8) and [eb, eb + 8), chosen so that eight pairs lie in
+// them.  The loads of a warp's first piece are issued before the angles and places are
+// known.
 template <int D, bool BWD, bool IL>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
   constexpr int UPH = D / 16;       // lanes per head
   constexpr int HPP = 32 / UPH;     // heads of a warp at once
-  constexpr int kBatch = 3;
   __shared__ Places pl;
   __shared__ int mark[32];
   __shared__ __align__(16) float cs[kMaxTile * kMaxHalf], sn[kMaxTile * kMaxHalf];
@@ -192,15 +193,13 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
   const int t0 = blockIdx.x * p.tile;
   const int n = min(p.tile, p.n_tokens - t0);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int wpt = p.tile < 8 ? 8 / p.tile : 1;
-  const int j_from = warp / wpt, j_step = 8 / wpt;
   const int u = lane % UPH;
   const bool turned = u < p.half / 8;
   const int ea = !IL && turned ? 8 * u : 16 * u;
   const int eb = !IL && turned ? ea + p.half : ea + 8;
-  const int kv_heads = 2 * p.Hkv, heads = kv_heads + p.Hq;
-  const int h_mine = warp % wpt * HPP + lane / UPH, h_step = wpt * HPP;
-  const int h_from = h_mine, h_to = BWD ? p.Hq : heads;  // backward: queries first
+  const int kv_heads = 2 * p.Hkv;
+  const int h_to = BWD ? p.Hq : kv_heads + p.Hq;  // backward: queries first
+  const int pieces = (h_to + HPP * p.batch - 1) / (HPP * p.batch);  // of a token
   uint4 xa[kBatch], xb[kBatch];
   auto load = [&](int j, int h0) {
     const size_t tok = t0 + j;
@@ -209,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
     const __nv_bfloat16* vrow = p.v + tok * p.v_stride - p.Hkv * D;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + i * h_step;
-      if (h < h_to) {
+      const int h = h0 + i * HPP;
+      if (i < p.batch && h < h_to) {
         const __nv_bfloat16* src =
             (BWD || h >= kv_heads ? qrow : h >= p.Hkv ? vrow : krow) + h * D;
         xa[i] = *reinterpret_cast<const uint4*>(src + ea);
@@ -218,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
       }
     }
   };
-  if (j_from < n) load(j_from, h_from);
+  int j = pieces > 0 ? warp / pieces : n, piece = warp - j * pieces;
+  if (j < n) load(j, piece * p.batch * HPP + lane / UPH);
 
   count_starts(p, t0, n, threadIdx.x <= p.n_seqs ? p.seq_start[threadIdx.x] : 0, mark);
   if (warp == 0) find_places(p, t0, n, &pl, mark, true);
@@ -228,67 +228,71 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
   __syncthreads();
 
   const size_t head_elems = static_cast<size_t>(p.P) * D;
-  for (int j = j_from; j < n; j += j_step) {
+  for (bool first = true; j < n; first = false) {
+    const int h0 = piece * p.batch * HPP + lane / UPH;
+    if (!first) load(j, h0);
     const size_t tok = t0 + j;
-    const int page = BWD ? 0 : pl.page[j];  // the backward needs it later, and registers now
     const bool used = pl.used[j];
     const float* cj = cs + j * p.half + 8 * u;
     const float* sj = sn + j * p.half + 8 * u;
-    // the token's row of KV head 0's keys in the pool
+    // forward: the token's row of KV head 0's keys in the pool
+    const int page = BWD ? 0 : pl.page[j];
     const size_t pool_row = BWD || page < 0 ? 0
                                             : static_cast<size_t>(page) * kv_heads * head_elems +
                                                   static_cast<size_t>(pl.row[j]) * D;
     __nv_bfloat16* orow = p.q_out + tok * p.q_out_stride - (BWD ? 0 : kv_heads * D);
-    for (int h0 = h_from; h0 < h_to; h0 += kBatch * h_step) {
-      if (j != j_from || h0 != h_from) load(j, h0);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * h_step;
-        if (h >= h_to) break;
-        const bool is_q = BWD || h >= kv_heads, is_v = !is_q && h >= p.Hkv;
-        if (is_q ? !used : page < 0) continue;
-        // blocks of a page: K and V of KV head 0, of KV head 1, ...
-        const int block = is_v ? 2 * (h - p.Hkv) + 1 : 2 * h;
-        const size_t at = pool_row + block * head_elems;
-        __nv_bfloat16* dst = is_q ? orow + h * D : p.kv + at;
-        if (turned && !is_v) {
-          float x[8], y[8];
-          unpack8(xa[i], x);
-          unpack8(xb[i], y);
-          rotate<BWD, IL>(x, y, cj, sj);
-          xa[i] = pack8(x);
-          xb[i] = pack8(y);
-        }
-        *reinterpret_cast<uint4*>(dst + ea) = xa[i];
-        *reinterpret_cast<uint4*>(dst + eb) = xb[i];
-        if (!BWD && !is_q && p.grad) {
-          float4* gz = reinterpret_cast<float4*>(p.grad + at);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) gz[u + e * UPH] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-    }
-    if (BWD && pl.page[j] >= 0) {
-      // the fp32 gradients of the token's keys and values
-      const float* grad_row = p.grad + static_cast<size_t>(pl.page[j]) * kv_heads * head_elems +
-                              static_cast<size_t>(pl.row[j]) * D;
-#pragma unroll 2
-      for (int h = h_mine; h < kv_heads; h += h_step) {
-        const bool is_v = h >= p.Hkv;
-        const float* src = grad_row + (is_v ? 2 * (h - p.Hkv) + 1 : 2 * h) * head_elems;
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * HPP;
+      if (i >= p.batch || h >= h_to) break;
+      const bool is_q = BWD || h >= kv_heads, is_v = !is_q && h >= p.Hkv;
+      if (is_q ? !used : page < 0) continue;
+      // blocks of a page: K and V of KV head 0, of KV head 1, ...
+      const int block = is_v ? 2 * (h - p.Hkv) + 1 : 2 * h;
+      const size_t at = pool_row + block * head_elems;
+      __nv_bfloat16* dst = is_q ? orow + h * D : p.kv + at;
+      if (turned && !is_v) {
         float x[8], y[8];
+        unpack8(xa[i], x);
+        unpack8(xb[i], y);
+        rotate<BWD, IL>(x, y, cj, sj);
+        xa[i] = pack8(x);
+        xb[i] = pack8(y);
+      }
+      *reinterpret_cast<uint4*>(dst + ea) = xa[i];
+      *reinterpret_cast<uint4*>(dst + eb) = xb[i];
+      if (!BWD && !is_q && p.grad) {
+        float4* gz = reinterpret_cast<float4*>(p.grad + at);
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(src + ea + e);
-          *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(src + eb + e);
-        }
-        if (turned && !is_v) rotate<BWD, IL>(x, y, cj, sj);
-        __nv_bfloat16* dst = is_v ? p.v + tok * p.v_stride + (h - p.Hkv) * D
-                                  : p.k + tok * p.k_stride + h * D;
-        *reinterpret_cast<uint4*>(dst + ea) = pack8(x);
-        *reinterpret_cast<uint4*>(dst + eb) = pack8(y);
+        for (int e = 0; e < 4; ++e) gz[u + e * UPH] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
+    for (piece += kThreads / 32; piece >= pieces; piece -= pieces) ++j;
+  }
+  if (!BWD) return;
+  // the fp32 gradients of the tokens' keys and values
+  const int rounds = (kv_heads + HPP - 1) / HPP;  // of a token
+#pragma unroll 2
+  for (int i = warp; i < n * rounds; i += kThreads / 32) {
+    j = i / rounds;
+    const int h = (i - j * rounds) * HPP + lane / UPH, page = pl.page[j];
+    if (h >= kv_heads || page < 0) continue;
+    const size_t tok = t0 + j;
+    const bool is_v = h >= p.Hkv;
+    const float* src = p.grad + static_cast<size_t>(page) * kv_heads * head_elems +
+                       (is_v ? 2 * (h - p.Hkv) + 1 : 2 * h) * head_elems +
+                       static_cast<size_t>(pl.row[j]) * D;
+    float x[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(src + ea + e);
+      *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(src + eb + e);
+    }
+    if (turned && !is_v) rotate<BWD, IL>(x, y, cs + j * p.half + 8 * u, sn + j * p.half + 8 * u);
+    __nv_bfloat16* dst = is_v ? p.v + tok * p.v_stride + (h - p.Hkv) * D
+                              : p.k + tok * p.k_stride + h * D;
+    *reinterpret_cast<uint4*>(dst + ea) = pack8(x);
+    *reinterpret_cast<uint4*>(dst + eb) = pack8(y);
   }
 }
 
@@ -442,6 +446,10 @@ oomb_status make_params(const oomb_pool* pool, const oomb_rope_args* a, bool bwd
   // one wave of the four CTAs that an SM holds
   const int slots = 4 * sm_count(d.device);
   p->tile = std::min(kMaxTile, (a->n_tokens + slots - 1) / slots);
+  // as many rounds of loads under way as leave each of a CTA's warps a piece
+  const int heads = p->Hq + (bwd ? 0 : 2 * d.num_kv_heads), at_once = 512 / d.head_dim;
+  const int rounds = p->tile * ((heads + at_once - 1) / at_once);
+  p->batch = std::min(kBatch, std::max(1, rounds / (kThreads / 32)));
   return OOMB_OK;
 }
 
