@@ -202,6 +202,8 @@ def _dev_tensor(t, dtype, name):
 
 def _arg(t, dtype, shape, dev, name):
     """Data pointer of a dense tensor of this type, shape (None: any) and device index."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype or t.get_device() != dev:
         raise TypeError(f"{name} must be {dtype} on cuda:{dev}, got {t.dtype} on {t.device}")
     got = t.shape
@@ -216,6 +218,8 @@ def _arg(t, dtype, shape, dev, name):
 def _rows(t, shape, dev, name):
     """(data pointer, elements from row to row) of bf16 [n][heads][head_dim] whose
     rows are dense but may stand apart, as the parts of a fused projection do."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not torch.bfloat16 or t.get_device() != dev:
         raise TypeError(f"{name} must be {torch.bfloat16} on cuda:{dev}, got {t.dtype} on "
                         f"{t.device}")
@@ -227,6 +231,14 @@ def _rows(t, shape, dev, name):
     if shape[0] <= 1:  # the distance of rows that are not there
         row = shape[1] * shape[2]
     return t.data_ptr(), row
+
+
+def _dim(t, i, name):
+    """A dimension of a tensor that _arg or _rows looks at later."""
+    try:
+        return t.shape[i]
+    except (AttributeError, IndexError):
+        raise TypeError(f"{name} must be a CUDA tensor of one dimension or more") from None
 
 
 def _stream_on(stream, dev):
@@ -360,18 +372,19 @@ def _rope_args(pool, k, v, seq_start, cached_lens, page_tables, positions, inv_f
                interleaved, names):
     dev, shape = _heads_of(k, names[0])
     n, H, D = shape
-    n_seqs = cached_lens.shape[0]
+    n_seqs = _dim(cached_lens, 0, "cached_lens")
     kp, ks = _rows(k, shape, dev, names[0])
     vp, vs = _rows(v, shape, dev, names[1])
     qp = qs = op = os_ = hq = 0
     if q is not None and q_out is not None:
-        hq = q.shape[1]
+        hq = _heads_of(q, names[2])[1][1]
         shape = (n, hq, D)
         qp, qs = _rows(q, shape, dev, names[2])
         op, os_ = _rows(q_out, shape, dev, names[3])
     elif q is not None or q_out is not None:
         raise ValueError(f"{names[2]} and {names[3]} go together")
-    i32, max_pages, half = torch.int32, page_tables.shape[-1], inv_freq.shape[0]
+    i32, max_pages = torch.int32, _dim(page_tables, -1, "page_tables")
+    half = _dim(inv_freq, 0, "inv_freq")
     return dev, _ROPE_PACK.pack(
         _arg(seq_start, i32, (n_seqs + 1,), dev, "seq_start"),
         _arg(cached_lens, i32, (n_seqs,), dev, "cached_lens"),
@@ -428,11 +441,11 @@ def decode_attn(pool, q, o, page_tables, seq_lens, softmax_scale, workspace, lse
     if prefix_pages is not None or prefix_lens is not None or group_start is not None:
         if prefix_pages is None or prefix_lens is None or group_start is None:
             raise ValueError("prefix_pages, prefix_lens and group_start go together")
-        ng, mp = prefix_lens.shape[0], prefix_pages.shape[-1]
+        ng, mp = _dim(prefix_lens, 0, "prefix_lens"), _dim(prefix_pages, -1, "prefix_pages")
         pp = _arg(prefix_pages, i32, (ng, mp), dev, "prefix_pages")
         pl = _arg(prefix_lens, i32, (ng,), dev, "prefix_lens")
         gs = _arg(group_start, i32, (ng + 1,), dev, "group_start")
-    max_pages, size = page_tables.shape[-1], workspace.shape[0]
+    max_pages, size = _dim(page_tables, -1, "page_tables"), _dim(workspace, 0, "workspace")
     a = _DECODE_PACK.pack(
         qp, op, lp, qs, os_, _arg(page_tables, i32, (n, max_pages), dev, "page_tables"),
         _arg(seq_lens, i32, (n,), dev, "seq_lens"), pp, pl, gs, n, hq, max_pages, ng, mp,

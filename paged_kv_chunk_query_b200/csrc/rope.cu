@@ -22,6 +22,7 @@ constexpr int kThreads = 256;
 constexpr int kMeanThreads = 512;
 constexpr int kMaxTile = 32; // tokens per CTA
 constexpr int kMaxHalf = 64; // pairs of a head
+constexpr int kMaxCount = 1 << 30;  // tokens, sequences: their sums with a tile stay in 32 bits
 constexpr int kBatch = 3;    // rounds of loads that a warp has under way
 
 struct RopeParams {
@@ -395,7 +396,8 @@ oomb_status make_params(const oomb_pool* pool, const oomb_rope_args* a, bool bwd
   const oomb_pool_desc& d = pool->desc;
   if (a->num_kv_heads != d.num_kv_heads || a->head_dim != d.head_dim || a->device != d.device)
     return OOMB_ERR_INVALID_ARG;
-  if (a->n_tokens < 0 || a->n_seqs < 0) return OOMB_ERR_INVALID_ARG;
+  if (a->n_tokens < 0 || a->n_seqs < 0 || a->n_tokens > kMaxCount || a->n_seqs > kMaxCount)
+    return OOMB_ERR_INVALID_ARG;
   if (bwd && !pool->grad) return OOMB_ERR_INVALID_ARG;
   if (a->rotary_dim < 0 || a->rotary_dim > d.head_dim || a->rotary_dim % 16)
     return OOMB_ERR_UNSUPPORTED;

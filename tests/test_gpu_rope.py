@@ -297,6 +297,7 @@ def test_refusals_leave_everything_untouched():
                            dict(q=None), dict(q_out=None), dict(k_stride=120), dict(v_stride=64),
                            dict(q_stride=252), dict(q_out_stride=8), dict(k=k.data_ptr() + 2),
                            dict(n_tokens=-1), dict(n_seqs=-1), dict(max_pages=0),
+                           dict(n_tokens=2**30 + 1), dict(n_seqs=2**31 - 1),
                            dict(num_q_heads=3), dict(num_q_heads=0), dict(interleaved=2),
                            dict(num_kv_heads=1), dict(head_dim=128), dict(device=1),
                            dict(q_out=q.data_ptr(), q_out_stride=512)):
@@ -317,6 +318,11 @@ def test_refusals_leave_everything_untouched():
             pk.kv_append_rope(pg.pool, k[..., :32], v[..., :32], *args)
         with pytest.raises(ValueError):
             pk.kv_append_rope(pg.pool, k, v, *args, q=q)
+        every = [k, v, *args, q, out]
+        for i in range(len(every)):  # no tensor, and one without dimensions
+            for wrong in (None, np.zeros(2, np.int32), every[i].reshape(-1)[0]):
+                with pytest.raises((TypeError, ValueError)):
+                    pk.kv_append_rope(pg.pool, *every[:i], wrong, *every[i + 1:])
         with pytest.raises(ValueError):
             pk.kv_append_rope(pg.pool, k, v, i32([0, 3, 6]), *args[1:])
         with pytest.raises(TypeError):
