@@ -259,7 +259,7 @@ oomb_status oomb_chunk_attn_bwd_step(oomb_pool* pool, const oomb_attn_args* args
  * not overlap.  q and q_out may both be NULL (num_q_heads is then ignored).
  * Requires a device pool; rotary_dim a multiple of 16 in [0, head_dim]
  * (OOMB_ERR_UNSUPPORTED otherwise; inv_freq may be NULL when it is 0).
- * n_tokens == 0 or n_seqs == 0 is a no-op. */
+ * n_tokens, n_seqs <= 2^30; n_tokens == 0 or n_seqs == 0 is a no-op. */
 typedef struct oomb_rope_args {
   const int32_t* seq_start;   /* device int32 [n_seqs + 1], ascending              */
   const int32_t* cached_lens; /* device int32 [n_seqs]                             */
@@ -304,9 +304,11 @@ oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args,
  * leaves [0, n_seqs] (which prefix its sequences then see is not specified); a
  * page id outside the pool sets bit 0 and its tokens are skipped.
  * Requires a device pool, num_q_heads a multiple of num_kv_heads, softmax_scale
- * > 0, n_seqs <= 65535, n_seqs * num_q_heads < 2^31, n_groups <= n_seqs, max_pages
+ * > 0 and finite, n_seqs <= 65535, n_seqs * num_q_heads < 2^31, n_groups <= n_seqs, max_pages
  * (and, with groups, max_prefix_pages) >= 1, rows of q and o dense [heads][head_dim],
- * 16-byte aligned, *_stride elements apart (a multiple of 8).  o may be q.
+ * 16-byte aligned, *_stride elements apart (a multiple of 8).  o may be q with
+ * the same stride.  A key of the sequence or its prefix whose score is NaN or
+ * +infinity makes the head's O and LSE NaN, as the formula does.
  * The workspace (oomb_decode_attn_workspace_size() bytes, 16-byte aligned) needs
  * no initialisation; calls sharing one must be ordered (one stream).  n_seqs ==
  * 0 is a no-op. */

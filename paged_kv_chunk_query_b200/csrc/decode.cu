@@ -21,6 +21,7 @@
 // of the others a CTA has at most two, the one it begins in and the one it ends
 // in, and writes them as parts into its two slots of the workspace.
 #include <algorithm>
+#include <cfloat>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -54,6 +55,7 @@ struct DecodeParams {
   int own_rows;   // query heads of a unit of own_kernel: 8 or 16
   int row_tiles;  // a sequence's units per KV head there
   int pre_in_own; // the prefixes are units of own_kernel too
+  int own_grid, pre_grid;  // CTAs of own_kernel, and of the kernel that takes the prefixes
   float scale_log2;
   // Workspace.  Part results are normalised O (fp32) and base-2 LSE.
   // own_meta [unit] {first CTA, CTAs}; slots [2 CTA + (0: begins before, 1: ends
@@ -675,11 +677,12 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
           const float2 x = *reinterpret_cast<const float2*>(&sl[n_units & 1][w][n * 8 + hd]);
           total = make_float2(total.x + x.x, total.y + x.y);
         }
-        const float i0 = total.x > 0.f ? __fdividef(1.f, total.x) : 0.f;
-        const float i1 = total.y > 0.f ? __fdividef(1.f, total.y) : 0.f;
+        // a sum is 0 without keys, and NaN (which stays) with a score of NaN or +inf
+        const float i0 = total.x != 0.f ? __fdividef(1.f, total.x) : 0.f;
+        const float i1 = total.y != 0.f ? __fdividef(1.f, total.y) : 0.f;
         if (warp == 0 && lane < 4) {
-          const float lse[2] = {total.x > 0.f ? m[n][0] + __log2f(total.x) : -INFINITY,
-                                total.y > 0.f ? m[n][1] + __log2f(total.y) : -INFINITY};
+          const float lse[2] = {total.x != 0.f ? m[n][0] + __log2f(total.x) : -INFINITY,
+                                total.y != 0.f ? m[n][1] + __log2f(total.y) : -INFINITY};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = n * 8 + hd + e;
@@ -1270,7 +1273,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (!(ok = warp_wait(&bar_fin[ln], n_units & 1, abort_flag))) break;
           ++n_units;
           tc_fence_after();
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = l != 0.f ? 1.f / l : 0.f;
           // half a row at a time through the place of the warp's own queries, which nothing
           // reads any more (other warps may be writing the next unit's into theirs): D / 8
           // lanes then write a row's half together
@@ -1307,7 +1310,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (valid)
           *(whole ? p.pre_row_lse[split ? ln : 0] + out_row : p.pre_slot_lse + slot_row) =
-              any && l > 0.f ? m_used + log2f(l) : -INFINITY;
+              any && l != 0.f ? m_used + log2f(l) : -INFINITY;
         tc_fence_before();  // these reads come before the next unit's products
       }
     }
@@ -1349,6 +1352,10 @@ __device__ __forceinline__ int find_group(const DecodeParams& p, int b) {
   return base >= 0 && base < p.n_groups ? base : -1;
 }
 
+__device__ __forceinline__ bool parts_in(int first, int n, int grid) {
+  return first >= 0 && n > 0 && first < grid && n <= grid - first;
+}
+
 // W warps per row (sequence, head); a lane takes 4 values of a part, a warp
 // 128 / D parts at once.
 template <int D, int W>
@@ -1379,6 +1386,9 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
   if (active) {
     own = p.own_meta[(static_cast<size_t>(b) * p.Hkv + h / p.G) * p.row_tiles + h % p.G / p.own_rows];
     if (n_pre) pre = p.pre_meta[row];
+    // a unit that its kernel gave up on (a wait ran out, the status word tells) has none
+    if (!parts_in(own.x, own.y, p.own_grid)) own = make_int2(0, 0);
+    if (!parts_in(pre.x, pre.y >> 1, p.pre_grid)) pre = make_int2(0, 0);
     // own_kernel has written this row already
     if (p.n_groups == 0 && own.y == 1) own.y = -1;
   }
@@ -1433,6 +1443,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
       if (k < n) {
         const Part r = part(k);
         lk[i] = *r.lse;
+        if (lk[i] != lk[i]) lk[i] = INFINITY;  // maxima drop NaN; inf - inf below is one again
         y[i] = *reinterpret_cast<const float4*>(r.o + d4);
       }
     }
@@ -1497,10 +1508,10 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
     }
   }
   if (!work || sub != 0) return;
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total != 0.f ? 1.f / total : 0.f;
   *reinterpret_cast<uint2*>(p.o + b * p.o_stride + h * D + d4) =
       make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-  if (lane == 0 && p.lse) p.lse[row] = total > 0.f ? kLn2 * (top + log2f(total)) : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[row] = total != 0.f ? kLn2 * (top + log2f(total)) : -INFINITY;
 }
 
 // ---------------------------------------------------------------- host
@@ -1554,7 +1565,9 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   p->pre_in_own = pre_in_own;
   p->own_rows = own_unit_rows(G, p->pre_in_own);
   p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
-  const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D, p->own_rows)) * p->own_rows;
+  p->own_grid = own_ctas(sms, D, p->own_rows);
+  const size_t own_rows = 2 * static_cast<size_t>(p->own_grid) * p->own_rows;
+  p->pre_grid = pre_in_own ? p->own_grid : sms;
   const size_t pre_rows = 4 * static_cast<size_t>(sms) * kPreTile;
   p->own_meta = reinterpret_cast<int2*>(take(static_cast<size_t>(n_seqs) * Hkv * p->row_tiles * 8));
   p->own_slot_o = reinterpret_cast<float*>(take(own_rows * D * 4));
@@ -1625,7 +1638,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   const bool prefix = p.n_groups > 0 && !p.pre_in_own;
   if (prefix) {
     if (!kv_map(&map, pool, p.P, 1)) return OOMB_ERR_CUDA;
-    cfg.gridDim = dim3(sms);
+    cfg.gridDim = dim3(p.pre_grid);
     cfg.blockDim = dim3(kPreThreads);
     cfg.dynamicSmemBytes = PreCfg<D>::kSmem;
     cfg.numAttrs = 0;
@@ -1633,7 +1646,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   }
   if (!kv_map(&map, pool, std::min(p.P, kOwnTile), 2)) return OOMB_ERR_CUDA;
   if (e == cudaSuccess) {
-    cfg.gridDim = dim3(own_ctas(sms, D, p.own_rows));
+    cfg.gridDim = dim3(p.own_grid);
     cfg.blockDim = dim3(kOwnThreads);
     cfg.numAttrs = prefix ? 1 : 0;
     cfg.dynamicSmemBytes = p.own_rows == 8 ? OwnCfg<D, 1>::kSmem : OwnCfg<D, 2>::kSmem;
@@ -1680,12 +1693,13 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   const int D = d.head_dim, Hq = a->num_q_heads;
   if (a->head_dim != D || a->device != d.device) return OOMB_ERR_INVALID_ARG;
   if (!good_shape(a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups)) return OOMB_ERR_INVALID_ARG;
-  if (!(a->softmax_scale > 0.f)) return OOMB_ERR_INVALID_ARG;
+  if (!(a->softmax_scale > 0.f && a->softmax_scale <= FLT_MAX)) return OOMB_ERR_INVALID_ARG;
   if (a->n_seqs == 0) return OOMB_OK;
   const int64_t width = static_cast<int64_t>(Hq) * D;
   if (!a->q || !a->o || !aligned16(a->q) || !aligned16(a->o) || a->q_stride % 8 ||
       a->o_stride % 8 || a->q_stride < width || a->o_stride < width)
     return OOMB_ERR_INVALID_ARG;
+  if (a->q == a->o && a->n_seqs > 1 && a->q_stride != a->o_stride) return OOMB_ERR_INVALID_ARG;
   if (a->max_pages <= 0 || !a->page_tables || !a->seq_lens) return OOMB_ERR_INVALID_ARG;
   if (a->n_groups > 0 &&
       (a->max_prefix_pages <= 0 || !a->prefix_pages || !a->prefix_lens || !a->group_start))

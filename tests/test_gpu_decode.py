@@ -201,6 +201,32 @@ def test_large_scores_one_key_dominates():
             b.check(*b.run())
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heads", [(28, 4, 128, 64), (4, 2, 64, 16)])
+@pytest.mark.parametrize("lens,groups", [
+    ([40, 65, 300], ()),                        # units whole and split
+    ([30000], ()),
+    ([20, 0, 90], [(0, 50), (2, None)]),        # groups of few rows, whole and split
+    ([20, 0, 90], [(0, 9000), (2, None)]),
+    ([1] * 40, [(0, 130), (39, None)]),         # of many rows
+    ([1] * 40, [(0, 20000), (39, None)]),
+])
+def test_a_key_that_is_not_finite_shows_in_its_rows_only(heads, lens, groups, bad):
+    with Batch(*heads, lens, groups, seed=23) as b:
+        want_o, want_l = b.run()
+        Hq, Hkv, d, P = heads
+        ids, n = (b.shared[0][0], b.pre[0]) if groups else (b.own[0][0], lens[0])
+        at = n // 2
+        # its score is NaN, or +inf: either way the softmax has no value
+        b.pg.kv[ids[at // P], 0, 0, at % P] = bad * torch.sign(b.q[0, 0].float()).to(b.q.dtype)
+        hit = torch.zeros(len(lens), Hq, dtype=torch.bool, device=DEV)
+        hit[slice(b.starts[0], b.starts[1]) if groups else 0, :Hq // Hkv] = True
+        o, lse = b.run()
+        assert torch.isnan(o[hit]).all(), torch.isnan(o[hit]).float().mean()
+        assert torch.isnan(lse[hit]).all()
+        assert torch.equal(o[~hit], want_o[~hit]) and torch.equal(lse[~hit], want_l[~hit])
+
+
 def test_same_bits_again_with_other_workspace_contents_and_a_larger_one():
     with Batch(28, 4, 128, 64, [900, 0, 77, 5000, 64], [(1, 2000), (4, None)], seed=4) as b:
         o, lse = b.run(ws=b.workspace(0))
@@ -351,6 +377,7 @@ def test_refusals_leave_everything_untouched():
                        dict(num_q_heads=0), dict(n_seqs=-1), dict(n_seqs=65536),
                        dict(n_groups=3), dict(n_groups=-1), dict(softmax_scale=0.0),
                        dict(softmax_scale=float("nan")), dict(workspace=None),
+                       dict(softmax_scale=float("inf")), dict(o=b.q.data_ptr(), o_stride=512),
                        dict(head_dim=128), dict(device=1),
                        dict(workspace=ws.data_ptr() + 4), dict(workspace_bytes=ws.numel() - 1)):
             assert call(**change) == L.ERR_INVALID_ARG, change
@@ -370,3 +397,8 @@ def test_refusals_leave_everything_untouched():
             pk.decode_attn(b.pg.pool, b.q, o, pages, lens.long(), 0.1, ws)
         with pytest.raises(TypeError):
             pk.decode_attn(b.pg.pool, b.q, o, pages.cpu(), lens, 0.1, ws)
+        args = [b.q, o, pages, lens, 0.1, ws]
+        for i in (0, 1, 2, 3, 5):  # no tensor, and one without dimensions
+            for wrong in (None, np.zeros(2, np.int32), args[i].reshape(-1)[0]):
+                with pytest.raises((TypeError, ValueError)):
+                    pk.decode_attn(b.pg.pool, *args[:i], wrong, *args[i + 1:])
