@@ -1352,10 +1352,6 @@ __device__ __forceinline__ int find_group(const DecodeParams& p, int b) {
   return base >= 0 && base < p.n_groups ? base : -1;
 }
 
-__device__ __forceinline__ bool parts_in(int first, int n, int grid) {
-  return first >= 0 && n > 0 && first < grid && n <= grid - first;
-}
-
 // W warps per row (sequence, head); a lane takes 4 values of a part, a warp
 // 128 / D parts at once.
 template <int D, int W>
@@ -1386,9 +1382,14 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
   if (active) {
     own = p.own_meta[(static_cast<size_t>(b) * p.Hkv + h / p.G) * p.row_tiles + h % p.G / p.own_rows];
     if (n_pre) pre = p.pre_meta[row];
-    // a unit that its kernel gave up on (a wait ran out, the status word tells) has none
-    if (!parts_in(own.x, own.y, p.own_grid)) own = make_int2(0, 0);
-    if (!parts_in(pre.x, pre.y >> 1, p.pre_grid)) pre = make_int2(0, 0);
+    // of a unit that its kernel gave up on (a wait ran out, the status word tells) they
+    // may say anything: no further than the slots go
+    own.x = min(max(own.x, 0), p.own_grid - 1);
+    own.y = min(max(own.y, 1), p.own_grid - own.x);
+    if (n_pre) {
+      pre.x = min(max(pre.x, 0), p.pre_grid - 1);
+      pre.y = min(max(pre.y, 2), 2 * (p.pre_grid - pre.x) + 1);
+    }
     // own_kernel has written this row already
     if (p.n_groups == 0 && own.y == 1) own.y = -1;
   }
