@@ -202,9 +202,11 @@ def _dev_tensor(t, dtype, name):
 
 def _arg(t, dtype, shape, dev, name):
     """Data pointer of a dense tensor of this type, shape (None: any) and device index."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype or t.get_device() != dev:
+    try:  # costs a tensor nothing, as asking for its type would
+        other = t.dtype is not dtype or t.get_device() != dev
+    except AttributeError:
+        raise TypeError(f"{name} must be a CUDA tensor") from None
+    if other:
         raise TypeError(f"{name} must be {dtype} on cuda:{dev}, got {t.dtype} on {t.device}")
     got = t.shape
     if got != shape and (len(got) != len(shape) or
@@ -218,9 +220,11 @@ def _arg(t, dtype, shape, dev, name):
 def _rows(t, shape, dev, name):
     """(data pointer, elements from row to row) of bf16 [n][heads][head_dim] whose
     rows are dense but may stand apart, as the parts of a fused projection do."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+    try:
+        other = t.dtype is not torch.bfloat16 or t.get_device() != dev
+    except AttributeError:
+        raise TypeError(f"{name} must be a CUDA tensor") from None
+    if other:
         raise TypeError(f"{name} must be {torch.bfloat16} on cuda:{dev}, got {t.dtype} on "
                         f"{t.device}")
     if t.shape != shape:
