@@ -55,7 +55,6 @@ struct DecodeParams {
   int own_rows;   // query heads of a unit of own_kernel: 8 or 16
   int row_tiles;  // a sequence's units per KV head there
   int pre_in_own; // the prefixes are units of own_kernel too
-  int own_grid, pre_grid;  // CTAs of own_kernel, and of the kernel that takes the prefixes
   float scale_log2;
   // Workspace.  Part results are normalised O (fp32) and base-2 LSE.
   // own_meta [unit] {first CTA, CTAs}; slots [2 CTA + (0: begins before, 1: ends
@@ -101,6 +100,10 @@ __device__ __forceinline__ Group group_of(const DecodeParams& p, int j, uint32_t
   r.len = checked_len(p.prefix_lens[j], p.max_prefix_pages, p.P, status);
   return r;
 }
+
+// The LSE of a part as the merge takes it: of parts it takes the maximum, which drops
+// NaN, so NaN goes as +inf, and exp(inf - inf) is NaN again.
+__device__ __forceinline__ float part_lse(float x) { return x != x ? INFINITY : x; }
 
 // Tiles of a length; an empty sequence of own_kernel has one (all masked) per unit,
 // which writes its result.
@@ -378,6 +381,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
         if (lane < p.max_pages) next_ids = p.page_tables[static_cast<size_t>(b) * p.max_pages + lane];
       }
     };
+    bool ok = true;
     if (n_mine > 0) {
       it.load(p, item, nullptr);
       look_ahead();
@@ -418,16 +422,16 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
         seq += d;
         head -= d * p.G;
       }
-      bool ok = true;
-      if (lane == 0) ok = mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, abort_flag);
+      // after a wait that ran out nothing is loaded any more, but the merge, which follows
+      // all the same, finds every unit's parts where it may look for them
+      if (ok && lane == 0) ok = mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
-      ++issued;
-      if (PRE) {
+      issued += ok;
+      if (PRE && ok) {
         if (last && lane < rows) out_rows[st][lane] = seq * p.Hq + head;
         __syncwarp();
       }
-      if (lane == 0) {
+      if (ok && lane == 0) {
         // the unit's first tile is this CTA's if it is not further back than its range
         const bool begins = i >= tile, ends = tile == it.nt - 1;
         TileInfo t;
@@ -442,10 +446,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
         mbar_arrive_expect_tx(&full[st], __popc(goods) * box_bytes + (first ? rows * D * 2 : 0));
       }
       __syncwarp();
-      if (good)
+      if (ok && good)
         tma_load_4d(ring + st * Cfg::kTileBytes + (hf * slots + s) * box_bytes, &kvmap, &full[st],
                     hf * 64, row0 & (p.P - 1), 2 * g, page);
-      if (first && lane < rows)
+      if (ok && first && lane < rows)
         bulk_load(sq + st * Cfg::kQBytes + lane * Cfg::kQRow, p.q + seq * p.q_stride + head * D, D * 2,
                   &full[st]);
       if (tile == 0) {
@@ -690,10 +694,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
             if (direct) {
               if (p.lse) p.lse[row0 + row] = kLn2 * lse[e];
             } else if (!whole) {
-              p.own_slot_lse[slot0 + row] = lse[e];
+              p.own_slot_lse[slot0 + row] = part_lse(lse[e]);
             } else {
               (PRE && pre ? p.pre_row_lse[0] : p.own_row_lse)[PRE ? out_rows[st][row] : row0 + row] =
-                  lse[e];
+                  part_lse(lse[e]);
             }
           }
         }
@@ -1123,6 +1127,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     size_t out_row = 0;
     int cnt = 0, n_s = 0, n_units = 0;
     bool ok = true, valid = false, begins = false, any = false;
+    int seq = 0, h = 0;
+    auto begin = [&] {  // this thread's row of the unit, and where its parts will be
+      const unsigned rr = (2u * w.pair + (w.split() ? 0 : ln)) * kPreTile + r;
+      const unsigned rs = rr / static_cast<unsigned>(p.G);
+      seq = w.gr.lo + static_cast<int>(rs);
+      h = w.g * p.G + static_cast<int>(rr - rs * p.G);
+      valid = seq < w.gr.hi;
+      begins = w.step == 0;
+      out_row = static_cast<size_t>(seq) * p.Hq + h;
+      if (valid && begins && (ln == 0 || !w.split()))
+        p.pre_meta[out_row] = make_int2(blockIdx.x, 2 * w.parts(per) + w.split());
+    };
     while (ok && w.next(p)) for (int i = 0; ok && i < w.here; ++i) {
       const bool split = w.split();
       const bool two = !split || w.tile(i, 1) < w.nt, extra = split && two;
@@ -1130,14 +1146,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       cnt += 2 + 2 * extra;
       const bool mine = ln == 0 || two;
       if (i == 0) {
-        // this thread's row of the unit
-        const unsigned rr = (2u * w.pair + (split ? 0 : ln)) * kPreTile + r;
-        const unsigned rs = rr / static_cast<unsigned>(p.G);
-        const int seq = w.gr.lo + static_cast<int>(rs);
-        const int h = w.g * p.G + static_cast<int>(rr - rs * p.G);
-        valid = seq < w.gr.hi;
-        begins = w.step == 0;
-        out_row = static_cast<size_t>(seq) * p.Hq + h;
+        begin();
         if (mine) {
           // its query into shared memory (A operand, K-major, 128-byte swizzle)
           const __nv_bfloat16* qrow = p.q + seq * p.q_stride + h * D;
@@ -1154,9 +1163,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_q[ln]);
-        }
-        if (valid && begins && (ln == 0 || !split)) {
-          p.pre_meta[out_row] = make_int2(blockIdx.x, 2 * w.parts(per) + split);
         }
         m_used = -INFINITY;
         l = 0.f;
@@ -1310,13 +1316,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (valid)
           *(whole ? p.pre_row_lse[split ? ln : 0] + out_row : p.pre_slot_lse + slot_row) =
-              any && l != 0.f ? m_used + log2f(l) : -INFINITY;
+              any && l != 0.f ? part_lse(m_used + log2f(l)) : -INFINITY;
         tc_fence_before();  // these reads come before the next unit's products
       }
     }
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) atomicOr(p.status, OOMB_DEV_WAIT_LIMIT);
+      while (w.next(p)) begin();  // the merge looks for these parts all the same
     }
   }
 
@@ -1382,14 +1389,6 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
   if (active) {
     own = p.own_meta[(static_cast<size_t>(b) * p.Hkv + h / p.G) * p.row_tiles + h % p.G / p.own_rows];
     if (n_pre) pre = p.pre_meta[row];
-    // of a unit that its kernel gave up on (a wait ran out, the status word tells) they
-    // may say anything: no further than the slots go
-    own.x = min(max(own.x, 0), p.own_grid - 1);
-    own.y = min(max(own.y, 1), p.own_grid - own.x);
-    if (n_pre) {
-      pre.x = min(max(pre.x, 0), p.pre_grid - 1);
-      pre.y = min(max(pre.y, 2), 2 * (p.pre_grid - pre.x) + 1);
-    }
     // own_kernel has written this row already
     if (p.n_groups == 0 && own.y == 1) own.y = -1;
   }
@@ -1444,7 +1443,6 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
       if (k < n) {
         const Part r = part(k);
         lk[i] = *r.lse;
-        if (lk[i] != lk[i]) lk[i] = INFINITY;  // maxima drop NaN; inf - inf below is one again
         y[i] = *reinterpret_cast<const float4*>(r.o + d4);
       }
     }
@@ -1566,9 +1564,7 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   p->pre_in_own = pre_in_own;
   p->own_rows = own_unit_rows(G, p->pre_in_own);
   p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
-  p->own_grid = own_ctas(sms, D, p->own_rows);
-  const size_t own_rows = 2 * static_cast<size_t>(p->own_grid) * p->own_rows;
-  p->pre_grid = pre_in_own ? p->own_grid : sms;
+  const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D, p->own_rows)) * p->own_rows;
   const size_t pre_rows = 4 * static_cast<size_t>(sms) * kPreTile;
   p->own_meta = reinterpret_cast<int2*>(take(static_cast<size_t>(n_seqs) * Hkv * p->row_tiles * 8));
   p->own_slot_o = reinterpret_cast<float*>(take(own_rows * D * 4));
@@ -1639,7 +1635,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   const bool prefix = p.n_groups > 0 && !p.pre_in_own;
   if (prefix) {
     if (!kv_map(&map, pool, p.P, 1)) return OOMB_ERR_CUDA;
-    cfg.gridDim = dim3(p.pre_grid);
+    cfg.gridDim = dim3(sms);
     cfg.blockDim = dim3(kPreThreads);
     cfg.dynamicSmemBytes = PreCfg<D>::kSmem;
     cfg.numAttrs = 0;
@@ -1647,7 +1643,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   }
   if (!kv_map(&map, pool, std::min(p.P, kOwnTile), 2)) return OOMB_ERR_CUDA;
   if (e == cudaSuccess) {
-    cfg.gridDim = dim3(p.own_grid);
+    cfg.gridDim = dim3(own_ctas(sms, D, p.own_rows));
     cfg.blockDim = dim3(kOwnThreads);
     cfg.numAttrs = prefix ? 1 : 0;
     cfg.dynamicSmemBytes = p.own_rows == 8 ? OwnCfg<D, 1>::kSmem : OwnCfg<D, 2>::kSmem;
