@@ -958,7 +958,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   volatile int* abort_flag = &abort_sh;
 
   if (warp >= 8) {
-    reg_dec<56>();
+    reg_dec<88>();
     if (warp == 8) {
       // ---------------------------------------------------------- loads
       PreWalk w;
@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_wait_drain(&bar_drain, 0);
     }
   } else {
-    reg_inc<224>();
+    reg_inc<208>();
     // ------------------------------------------------------------ softmax
     const int ln = warp / 4, r = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
