@@ -268,6 +268,12 @@ struct TileInfo {
 // tiles by TMA (K and V of a page and head are neighbours in the pool: one box of
 // both per 64 columns).  The number of barriers does not depend on what is found, so
 // a wait that gives up leaves nobody behind.
+// Bound by memory where sequences are long: 3 x 100-131 thousand keys (745 MB) take
+// 113-116 us, 6.4-6.6 TB/s.  A ragged batch (48 sequences, 103 MB) takes 22.3-23.0 us
+// alone, 4.5 TB/s: CTAs have 7 tiles each, and their start, the look at lengths and pages,
+// takes as long as three.  Three CTAs of two tiles each keep more loads under way than two
+// of three (22.6 and 24.6 us); a separate warp for a unit's end costs the registers that
+// the third CTA needs.
 //
 // PRE: the prefixes' keys are units too, of up to kRows rows (sequence, query head)
 // of a group; items [0, n_groups) are groups, the others sequences.  A sequence is
@@ -906,6 +912,13 @@ __device__ __forceinline__ void reg_dec() {
 // the lane looks at them.  TMEM columns: S of lane 0 and 1 [0,128) [128,256) (P in
 // their first half), O [256,384) [384,512).  Q is in shared memory, written by its
 // lane's threads.
+// Bound by the tensor cores' clock and the chain of a step for many rows: 256 sequences
+// behind 32773 tokens (1792 rows per KV head, 120 GFLOP) take about 125 us at 1.6 GHz
+// (1.9 without this load), 960 TFLOP/s.  No one part holds it up: without the exponentials
+// the call takes 127 instead of 135 us, without the loads 129, with an eighth of the PV
+// products 131.  Two threads per row (139), exponentials by a polynomial for a part of the
+// row (137-164), asking for barriers ahead of time (168) and a product warp per lane (174)
+// were slower.
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1)
     prefix_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kvmap) {
@@ -958,6 +971,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   volatile int* abort_flag = &abort_sh;
 
   if (warp >= 8) {
+    // 208 and 88 registers: with 224 and 56 (216 and 72) these warps spill, to L2, as shared
+    // memory leaves no L1: 256 sequences behind 32773 tokens 145 (145) us, now 135; with 200
+    // and 104 the softmax does, 138 us
     reg_dec<88>();
     if (warp == 8) {
       // ---------------------------------------------------------- loads
@@ -1360,7 +1376,10 @@ __device__ __forceinline__ int find_group(const DecodeParams& p, int b) {
 }
 
 // W warps per row (sequence, head); a lane takes 4 values of a part, a warp
-// 128 / D parts at once.
+// 128 / D parts at once.  Bound by latency: its launch (a dependent one), the look for a
+// row's parts, then the parts, four at a time.  Alone 6.3-6.9 us with 84 rows of up to 150
+// parts (W 16) or 1344 rows (W 4), 15 us with 7168 rows of about 10 parts from DRAM
+// (W 1, 27 MB); in a call the parts come from L2.
 template <int D, int W>
 __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const DecodeParams p) {
   constexpr int TPR = D / 4, PPW = 32 / TPR;
