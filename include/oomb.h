@@ -241,7 +241,7 @@ oomb_status oomb_chunk_attn_bwd_step(oomb_pool* pool, const oomb_attn_args* args
  *   negative cached_lens and a seq_start that decreases or leaves [0, n_tokens]
  *   set bit 2.  Such tokens' keys and values are skipped.
  * Two tokens of one call must not share a cache position, and pages that one
- * call writes must belong to one sequence each.  Two launches.
+ * call writes must belong to one sequence each.  One or two launches.
  *
  * oomb_kv_append_rope_bwd: its backward, the step between attention's
  * gradients and the projection's: for the same tokens,

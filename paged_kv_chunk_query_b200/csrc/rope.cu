@@ -1,7 +1,8 @@
 // kv_append_rope: keys and values of a ragged batch of tokens into the pages of
 // their sequences, keys and queries rotated by their positions on the way; and
 // its backward, which takes the paged fp32 gradients out token-major and
-// rotates them back.
+// rotates them back.  Page means: by the same CTAs for few tokens per sequence, else by
+// a second, dependent launch (page_mean_kernel).
 //
 // Rotation of pair i of a token at position p by the angle a = p f_i:
 //   y_a = x_a cos a - x_b sin a,   y_b = x_b cos a + x_a sin a,
@@ -20,6 +21,7 @@ using namespace oomb;
 
 constexpr int kThreads = 256;
 constexpr int kMeanThreads = 512;
+constexpr int kMeanCtas = 3;  // per SM, of one token each, that take page means too
 constexpr int kMaxTile = 32; // tokens per CTA
 constexpr int kMaxHalf = 64; // pairs of a head
 constexpr int kMaxCount = 1 << 30;  // tokens, sequences: their sums with a tile stay in 32 bits
@@ -58,6 +60,7 @@ struct Places {
   int page[32];  // physical page; < 0: the token is not written
   int row[32];
   int last[32];  // it is the last token that this call puts into its page
+  int first[32]; // row of the first one
   int used[32];  // the token belongs to a sequence (its queries are rotated)
 };
 
@@ -92,7 +95,7 @@ __device__ __forceinline__ void find_places(const RopeParams& p, int t0, int n, 
     if (t >= d) seq += v;
   }
   --seq;
-  int page = -1, row = 0, last = 0, used = 0;
+  int page = -1, row = 0, last = 0, first = 0, used = 0;
   if (t < n && seq >= 0 && seq < p.n_seqs) {
     const int tok = t0 + t, lo = p.seq_start[seq], hi = p.seq_start[seq + 1];
     const int cached = p.cached_lens[seq];
@@ -109,6 +112,7 @@ __device__ __forceinline__ void find_places(const RopeParams& p, int t0, int n, 
         row = static_cast<int>(c) & (p.P - 1);
         page = p.page_tables[static_cast<size_t>(seq) * p.max_pages + pi];
         last = row == p.P - 1 || tok + 1 == hi;
+        first = static_cast<int>(max(cached - (pi << p.lg_p), 0ll));
         if (page < 0 || page >= p.num_pages) {
           bad = OOMB_DEV_BAD_PAGE;
           page = -1;
@@ -120,6 +124,7 @@ __device__ __forceinline__ void find_places(const RopeParams& p, int t0, int n, 
   out->page[t] = page;
   out->row[t] = row;
   out->last[t] = last;
+  out->first[t] = first;
   out->used[t] = used;
 }
 
@@ -177,6 +182,110 @@ __device__ __forceinline__ void rotate(float* x, float* y, const float* cs, cons
   }
 }
 
+// The representative of the page into which token `tok` goes, row `row`, the last row
+// written by this call: the mean of the keys of rows [0, row].  Rows from `first` on are
+// this call's, possibly written by other CTAs: their keys are rotated anew from the
+// inputs, the others read from the page.  All threads of a CTA: a KV head has `share`
+// warps, a row UPH lanes as in rope_kernel.  cs, sn: the token's angles, and place for those
+// of kMaxTile tokens.
+template <int D, bool IL>
+__device__ __forceinline__ void mean_of_page(const RopeParams& p, int tok, int page, int row,
+                                             int first, float* cs, float* sn) {
+  constexpr int UPH = D / 16, RPW = 32 / UPH, kWarps = kThreads / 32;
+  constexpr int kRows = 4;  // rows under way per lane
+  __shared__ __align__(16) float red[kWarps][D];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int u = lane % UPH, sub = lane / UPH;
+  const bool turned = u < p.half / 8;
+  const int ea = !IL && turned ? 8 * u : 16 * u;
+  const int eb = !IL && turned ? ea + p.half : ea + 8;
+  int share = 1;
+  while (2 * share <= kWarps && 2 * share * p.Hkv <= kWarps) share *= 2;
+  const int part = warp % share, step = share * RPW;
+  auto add = [](float* acc, const uint4& v) {
+    float x[8];
+    unpack8(v, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += x[e];
+  };
+  auto sum_stored = [&](int g, float* ax, float* ay) {  // rows [0, first)
+    const __nv_bfloat16* src = p.kv + (static_cast<size_t>(page) * p.Hkv + g) * 2 * p.P * D;
+    for (int r0 = part * RPW + sub; r0 < first; r0 += kRows * step) {
+      uint4 a[kRows], b[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (r0 + i * step < first) {
+          a[i] = *reinterpret_cast<const uint4*>(src + (r0 + i * step) * D + ea);
+          b[i] = *reinterpret_cast<const uint4*>(src + (r0 + i * step) * D + eb);
+        }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (r0 + i * step >= first) break;
+        add(ax, a[i]);
+        add(ay, b[i]);
+      }
+    }
+  };
+  auto sum_new = [&](int g, int from, int to, float* ax, float* ay) {  // their angles in cs, sn
+    for (int r = from + part * RPW + sub; r < to; r += step) {
+      const __nv_bfloat16* src = p.k + (static_cast<int64_t>(tok) - row + r) * p.k_stride + g * D;
+      uint4 a = *reinterpret_cast<const uint4*>(src + ea), b = *reinterpret_cast<const uint4*>(src + eb);
+      if (turned) {
+        float x[8], y[8];
+        unpack8(a, x);
+        unpack8(b, y);
+        const int at = (r - from) * p.half + 8 * u;
+        rotate<false, IL>(x, y, cs + at, sn + at);
+        a = pack8(x);  // as stored
+        b = pack8(y);
+      }
+      add(ax, a);
+      add(ay, b);
+    }
+  };
+  const int g = warp / share;  // Hkv <= kWarps
+  const bool active = g < p.Hkv;
+  float x[8], y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+  if (active) {
+    sum_stored(g, x, y);
+    if (first == row) sum_new(g, row, row + 1, x, y);
+  }
+  if (first < row) {  // angles of kMaxTile rows at a time
+    for (int r = first; r <= row; r += kMaxTile) {
+      const int to = min(row + 1, r + kMaxTile);
+      __syncthreads();
+      for (int i = threadIdx.x; i < (to - r) * p.half; i += kThreads)
+        turn(p.positions[tok - row + r + i / p.half], p.inv_freq[i % p.half], cs + i, sn + i);
+      __syncthreads();
+      if (active) sum_new(g, r, to, x, y);
+    }
+  }
+#pragma unroll
+  for (int m = UPH; m < 32; m *= 2)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] += __shfl_xor_sync(0xffffffffu, x[e], m);
+      y[e] += __shfl_xor_sync(0xffffffffu, y[e], m);
+    }
+  if (sub == 0) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      *reinterpret_cast<float4*>(red[warp] + ea + e) = *reinterpret_cast<const float4*>(x + e);
+      *reinterpret_cast<float4*>(red[warp] + eb + e) = *reinterpret_cast<const float4*>(y + e);
+    }
+  }
+  __syncthreads();
+  const float n = static_cast<float>(row + 1);
+  for (int i = threadIdx.x; i < p.Hkv * D; i += kThreads) {
+    const int w = i / D, e = i % D;
+    float total = red[w * share][e];
+    for (int k = 1; k < share; ++k) total += red[w * share + k][e];
+    p.summary[static_cast<size_t>(page) * p.Hkv * D + i] = total / n;
+  }
+}
+
 // One CTA: `tile` <= 32 tokens.  A warp takes heads of a token (counted K, V, then Q)
 // 32 / (D / 16) at a time, `batch` <= kBatch times; these pieces of all the CTA's
 // tokens are dealt out to its warps in turn.  A lane has the same two 16-byte vectors
@@ -188,14 +297,16 @@ __device__ __forceinline__ void rotate(float* x, float* y, const float* cs, cons
 // this stand the start (places and angles, about 3 us before the first store) and the
 // issue slots (57% used).  One wave of CTAs, four per SM: three, or seven warps each so
 // that the mean kernel fits beside, were slower (24.6 us with the means, now 20.5).
-template <int D, bool BWD, bool IL>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
+//
+// MEAN (CTAs of one token): the page means too, see mean_of_page.
+template <int D, bool BWD, bool IL, bool MEAN>
+__global__ void __launch_bounds__(kThreads, MEAN ? kMeanCtas : 4) rope_kernel(const RopeParams p) {
   constexpr int UPH = D / 16;       // lanes per head
   constexpr int HPP = 32 / UPH;     // heads of a warp at once
   __shared__ Places pl;
   __shared__ int mark[32];
   __shared__ __align__(16) float cs[kMaxTile * kMaxHalf], sn[kMaxTile * kMaxHalf];
-  if (!BWD) pdl_launch_dependents();
+  if (!BWD && !MEAN) pdl_launch_dependents();
   const int t0 = blockIdx.x * p.tile;
   const int n = min(p.tile, p.n_tokens - t0);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -275,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
     }
     for (piece += kThreads / 32; piece >= pieces; piece -= pieces) ++j;
   }
+  if (MEAN && pl.last[0] && pl.page[0] >= 0)
+    mean_of_page<D, IL>(p, t0, pl.page[0], pl.row[0], pl.first[0], cs, sn);
   if (!BWD) return;
   // the fp32 gradients of the tokens' keys and values
   const int rounds = (kv_heads + HPP - 1) / HPP;  // of a token
@@ -463,15 +576,15 @@ oomb_status make_params(const oomb_pool* pool, const oomb_rope_args* a, bool bwd
   return OOMB_OK;
 }
 
-template <bool BWD>
+template <bool BWD, bool MEAN>
 void launch_rope(const RopeParams& p, int D, cudaStream_t s) {
   const int grid = (p.n_tokens + p.tile - 1) / p.tile;
   if (D == 128) {
-    if (p.interleaved) rope_kernel<128, BWD, true><<<grid, kThreads, 0, s>>>(p);
-    else rope_kernel<128, BWD, false><<<grid, kThreads, 0, s>>>(p);
+    if (p.interleaved) rope_kernel<128, BWD, true, MEAN><<<grid, kThreads, 0, s>>>(p);
+    else rope_kernel<128, BWD, false, MEAN><<<grid, kThreads, 0, s>>>(p);
   } else {
-    if (p.interleaved) rope_kernel<64, BWD, true><<<grid, kThreads, 0, s>>>(p);
-    else rope_kernel<64, BWD, false><<<grid, kThreads, 0, s>>>(p);
+    if (p.interleaved) rope_kernel<64, BWD, true, MEAN><<<grid, kThreads, 0, s>>>(p);
+    else rope_kernel<64, BWD, false, MEAN><<<grid, kThreads, 0, s>>>(p);
   }
 }
 
@@ -485,7 +598,18 @@ extern "C" oomb_status oomb_kv_append_rope(oomb_pool* pool, const oomb_rope_args
   const oomb_pool_desc& d = pool->desc;
   DeviceGuard guard(d.device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  launch_rope<false>(p, d.head_dim, s);
+  // Few tokens per sequence, one CTA each, take the page means in the same launch: a page
+  // then has few new rows to be rotated a second time.  One launch and two, with the time of
+  // a call from Python (device alone in brackets): 64 x 1 token, 28 and 4 heads of 128, 10.2
+  // (6.2) and 11.9 us (8.2); 50 x 8 tokens 9.9 (8.7) and 12.7 (10.3); 300 x 1, 8 KV heads,
+  // 128-token pages 14.4 (14.4) and 16.2 (16.1).  One prompt of 440 tokens 14.8 and 12.1;
+  // with 16 KV heads a CTA has two per warp: 200 x 2 tokens 25.5 and 20.0.
+  if (p.n_tokens <= kMeanCtas * sm_count(d.device) && p.n_tokens / 8 <= p.n_seqs &&
+      p.Hkv <= kThreads / 32) {
+    launch_rope<false, true>(p, d.head_dim, s);
+    return check_launch();
+  }
+  launch_rope<false, false>(p, d.head_dim, s);
   // page means: a dependent launch, its search for the pages runs beside the rotation
   const int slots = 2 * sm_count(d.device);
   p.tile = std::min(32, (p.n_tokens + slots - 1) / slots);
@@ -513,6 +637,6 @@ extern "C" oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_
   oomb_status st = make_params(pool, args, true, &p);
   if (st != OOMB_OK || args->n_tokens == 0 || args->n_seqs == 0) return st;
   DeviceGuard guard(pool->desc.device);
-  launch_rope<true>(p, pool->desc.head_dim, static_cast<cudaStream_t>(stream));
+  launch_rope<true, false>(p, pool->desc.head_dim, static_cast<cudaStream_t>(stream));
   return check_launch();
 }

@@ -48,6 +48,11 @@ CASES = [
     (5, 5, 128, 16, 0, False, [20, 1], [3, 16], 9),
     (2, 2, 64, 32, 64, True, [1] * 300, [i % 70 for i in range(300)], 100),
     (4, 2, 128, 64, 64, False, [1500, 700], [10, 0], 1000),
+    # few tokens per sequence, one with many: its pages' rows come from many blocks
+    (6, 3, 128, 128, 64, True, [2, 200, 0, 1] + [1] * 40, [5, 100, 3, 127] + [9 * i for i in range(40)], 7),
+    (8, 8, 64, 32, 64, False, [1, 0, 3, 70] + [2] * 20, [31, 2, 0, 60] + [i for i in range(20)], 2**20),
+    (5, 5, 128, 16, 128, False, [40] + [0] * 9 + [1], [8] + [0] * 9 + [15], 3),
+    (16, 16, 64, 16, 32, False, [2, 1, 1], [15, 0, 30], 50),
 ]
 
 
