@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, MEAN ? kMeanCtas : 4) rope_kernel(co
 // few of them: the load latency of 64 rows is then paid once.  Bound by latency: 8.4-9.0 us
 // alone for a chunk of 4096 tokens, about 5 behind rope_kernel.  A single launch in which a
 // CTA owns a page's keys and values needs none of this, but is uneven: the chunk took
-// 28-30 us, 64 single tokens 12-14 instead of 8.2.
+// 28-30 us.  A ticket per page, by which the last of its CTAs takes the mean, is no faster
+// (the chunk 18.5 us both ways, with 16 KV heads of 128-token pages 40 instead of 30).
 template <int D>
 __global__ void __launch_bounds__(kMeanThreads, 2) page_mean_kernel(const RopeParams p) {
   constexpr int VPR = D / 8;      // 16-byte vectors per row
