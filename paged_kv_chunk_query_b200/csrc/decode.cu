@@ -346,10 +346,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
     }
     fence_mbar_init();
   }
-  // heads past the unit's last stay zero: their scores would be NaN by chance
-  for (int i = threadIdx.x * 16; i < Cfg::kStages * Cfg::kQBytes; i += kOwnThreads * 16)
-    *reinterpret_cast<uint4*>(sq + i) = make_uint4(0, 0, 0, 0);
-  fence_async_smem();
   const int n_items = (PRE ? p.n_groups : 0) + p.n_seqs;
   const Range rg = find_range<kOwnThreads, 0>(n_items, [&](int i, bool note) {
     Item it;
@@ -534,6 +530,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
             ldsm4(sq_at + st * Cfg::kQBytes + (n * 8 + (lane & 7)) * Cfg::kQRow + kk * 32 +
                       (lane >> 3) * 16,
                   qf[n][kk]);
+          // rows past the unit's last hold what an earlier unit left: as zeros they ask for no
+          // rescaling of the others
+          if (n * 8 + lane / 4 >= t.rows)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) qf[n][kk][0] = qf[n][kk][1] = 0;
 #pragma unroll
           for (int c = 0; c < MT; ++c)
 #pragma unroll

@@ -402,3 +402,16 @@ def test_refusals_leave_everything_untouched():
             for wrong in (None, np.zeros(2, np.int32), args[i].reshape(-1)[0]):
                 with pytest.raises((TypeError, ValueError)):
                     pk.decode_attn(b.pg.pool, *args[:i], wrong, *args[i + 1:])
+
+
+@pytest.mark.parametrize("d,P", [(128, 64), (64, 16)])
+def test_heads_of_another_unit_do_not_show(d, P):
+    """24 heads of a KV head are units of 16 and 8 rows on the same thread block: what the
+    first 16 ask for has no part in the other 8, not even in when their sums are rescaled."""
+    with Batch(24, 1, d, P, [128] * 600, seed=31) as b:
+        o, lse = b.run()
+        for change in (30.0, float("nan")):
+            q = b.q.clone()
+            q[:, 8:16] *= change
+            o2, lse2 = b.run(q=q)
+            assert torch.equal(o[:, 16:], o2[:, 16:]) and torch.equal(lse[:, 16:], lse2[:, 16:])
