@@ -304,7 +304,8 @@ oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args,
  * leaves [0, n_seqs] (which prefix its sequences then see is not specified); a
  * page id outside the pool sets bit 0 and its tokens are skipped.
  * Requires a device pool, num_q_heads a multiple of num_kv_heads, softmax_scale
- * > 0 and finite, n_seqs <= 65535, n_seqs * num_q_heads < 2^31, n_groups <= n_seqs, max_pages
+ * > 0 and finite in fp32 also after a multiplication by log2(e), n_seqs <= 65535,
+ * n_seqs * num_q_heads < 2^31, n_groups <= n_seqs, max_pages
  * (and, with groups, max_prefix_pages) >= 1, rows of q and o dense [heads][head_dim],
  * 16-byte aligned, *_stride elements apart (a multiple of 8).  o may be q with
  * the same stride.  A key of the sequence or its prefix whose score is NaN or

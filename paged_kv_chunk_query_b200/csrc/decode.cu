@@ -1710,7 +1710,9 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   const int D = d.head_dim, Hq = a->num_q_heads;
   if (a->head_dim != D || a->device != d.device) return OOMB_ERR_INVALID_ARG;
   if (!good_shape(a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups)) return OOMB_ERR_INVALID_ARG;
-  if (!(a->softmax_scale > 0.f && a->softmax_scale <= FLT_MAX)) return OOMB_ERR_INVALID_ARG;
+  // the exponentials are powers of 2: an infinite factor would make scores of 0 NaN
+  const float scale_log2 = a->softmax_scale * kLog2e;
+  if (!(a->softmax_scale > 0.f && scale_log2 <= FLT_MAX)) return OOMB_ERR_INVALID_ARG;
   if (a->n_seqs == 0) return OOMB_OK;
   const int64_t width = static_cast<int64_t>(Hq) * D;
   if (!a->q || !a->o || !aligned16(a->q) || !aligned16(a->o) || a->q_stride % 8 ||
@@ -1751,7 +1753,7 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
   p.n_groups = a->n_groups;
   p.max_prefix_pages = a->max_prefix_pages;
   p.num_pages = d.num_pages;
-  p.scale_log2 = a->softmax_scale * kLog2e;
+  p.scale_log2 = scale_log2;
   DeviceGuard guard(d.device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return D == 128 ? launch<128>(pool, p, sms, s) : launch<64>(pool, p, sms, s);

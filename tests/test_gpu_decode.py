@@ -415,3 +415,22 @@ def test_heads_of_another_unit_do_not_show(d, P):
             q[:, 8:16] *= change
             o2, lse2 = b.run(q=q)
             assert torch.equal(o[:, 16:], o2[:, 16:]) and torch.equal(lse[:, 16:], lse2[:, 16:])
+
+
+def test_scale_that_overflows_in_powers_of_two_is_refused():
+    """Scores of 0 under the largest scales are a plain mean, or the call is refused."""
+    with Batch(4, 2, 64, 16, [40, 20], seed=32) as b:
+        b.q.zero_()
+        o, lse = b.run()
+        pages, lens, _ = b.args()
+        o2 = torch.empty_like(o)
+        pk.decode_attn(b.pg.pool, b.q, o2, pages, lens, 2.35e38, b.workspace())
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2)
+        # the largest fp32 number / log2(e) = 2.3586e38
+        for scale in (2.36e38, 3.4e38):
+            o2 = torch.full_like(o, 5.0)
+            with pytest.raises(pk.OombError):
+                pk.decode_attn(b.pg.pool, b.q, o2, pages, lens, scale, b.workspace())
+            torch.cuda.synchronize()
+            assert (o2 == 5.0).all()
