@@ -450,10 +450,13 @@ def decode_attn(pool, q, o, page_tables, seq_lens, softmax_scale, workspace, lse
         pl = _arg(prefix_lens, i32, (ng,), dev, "prefix_lens")
         gs = _arg(group_start, i32, (ng + 1,), dev, "group_start")
     max_pages, size = _dim(page_tables, -1, "page_tables"), _dim(workspace, 0, "workspace")
-    a = _DECODE_PACK.pack(
-        qp, op, lp, qs, os_, _arg(page_tables, i32, (n, max_pages), dev, "page_tables"),
-        _arg(seq_lens, i32, (n,), dev, "seq_lens"), pp, pl, gs, n, hq, max_pages, ng, mp,
-        softmax_scale, _arg(workspace, torch.uint8, (size,), dev, "workspace"), size, D, dev)
+    try:
+        a = _DECODE_PACK.pack(
+            qp, op, lp, qs, os_, _arg(page_tables, i32, (n, max_pages), dev, "page_tables"),
+            _arg(seq_lens, i32, (n,), dev, "seq_lens"), pp, pl, gs, n, hq, max_pages, ng, mp,
+            softmax_scale, _arg(workspace, torch.uint8, (size,), dev, "workspace"), size, D, dev)
+    except struct.error as e:  # the one value here that is neither a pointer nor a shape
+        raise TypeError(f"softmax_scale must be a number, got {softmax_scale!r} ({e})") from None
     _check(load().oomb_decode_attn(pool, a, _stream_on(stream, dev)), "oomb_decode_attn")
 
 

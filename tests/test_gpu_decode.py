@@ -434,3 +434,12 @@ def test_scale_that_overflows_in_powers_of_two_is_refused():
                 pk.decode_attn(b.pg.pool, b.q, o2, pages, lens, scale, b.workspace())
             torch.cuda.synchronize()
             assert (o2 == 5.0).all()
+
+
+def test_scale_that_is_no_number_is_a_type_error():
+    with Batch(4, 2, 64, 16, [40, 20], seed=33) as b:
+        pages, lens, _ = b.args()
+        for scale in (None, "0.1", [0.1]):
+            with pytest.raises(TypeError):
+                pk.decode_attn(b.pg.pool, b.q, torch.empty_like(b.q), pages, lens, scale,
+                               b.workspace())
