@@ -33,6 +33,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "tiles.cuh"
 #include "tmap.h"
@@ -568,13 +569,6 @@ __global__ void __launch_bounds__(128) fwd_merge_kernel(const FwdParams p) {
   // every lane of the row has read the old lse before it is replaced
   __syncwarp();
   if (active && seg == 0) *lse_ptr = lse_out;
-}
-
-int sm_count(int device) {
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0)
-    n = 148;
-  return n;
 }
 
 template <int D>

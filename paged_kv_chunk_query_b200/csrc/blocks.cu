@@ -20,25 +20,19 @@
 // Entries with a negative id are padding and skipped; an id beyond its pool
 // sets the device status bit and is skipped.
 #include "internal.h"
+#include "launch.cuh"
 
 namespace {
 
 constexpr int kMoveThreads = 256;
 constexpr int kUnroll = 4;  // 16-byte accesses in flight per thread
 
-int sm_count(int device) {
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0)
-    n = 148;
-  return n;
-}
-
 // grid size: a few CTAs already saturate the host link (measured on B200:
 // 8 CTAs copy at 51 GB/s, 16 add at 40 GB/s each way), and fewer CTAs leave
 // more SMs to the attention kernels these moves run beside; an HBM gather
 // wants several CTAs per SM.
 int move_grid(int n_blocks, bool over_host_link, bool read_modify_write, int device) {
-  const int cap = over_host_link ? (read_modify_write ? 16 : 8) : 4 * sm_count(device);
+  const int cap = over_host_link ? (read_modify_write ? 16 : 8) : 4 * oomb::sm_count(device);
   return n_blocks < cap ? n_blocks : cap;
 }
 

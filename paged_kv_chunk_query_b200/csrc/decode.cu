@@ -24,6 +24,7 @@
 #include <cfloat>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "tmap.h"
 
@@ -73,11 +74,6 @@ struct DecodeParams {
   float* pre_row_o[2];
   float* pre_row_lse[2];
 };
-
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A length, clamped to what its page table holds.
 __device__ __forceinline__ int checked_len(int len, int max_pages, int P, uint32_t* status) {
@@ -1534,15 +1530,6 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
 }
 
 // ---------------------------------------------------------------- host
-int sm_count(int device) {
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    n = 148;
-  }
-  return n;
-}
-
 bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_groups) {
   return n_seqs >= 0 && n_seqs <= 65535 && Hkv > 0 && Hq > 0 && Hq % Hkv == 0 &&
          supported_head_dim(D) && n_groups >= 0 && n_groups <= n_seqs &&

@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace {
@@ -49,11 +50,6 @@ struct RopeParams {
   int tile;         // tokens per CTA
   int batch;        // rounds of heads per piece, at most kBatch
 };
-
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Where the tokens [t0, t0 + n) of a CTA go.
 struct Places {
@@ -500,13 +496,6 @@ __global__ void __launch_bounds__(kMeanThreads, 2) page_mean_kernel(const RopePa
       dst[1] = make_float4(acc[4] / k, acc[5] / k, acc[6] / k, acc[7] / k);
     }
   }
-}
-
-int sm_count(int device) {
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0)
-    n = 148;
-  return n;
 }
 
 bool good_rows(const void* p, int64_t stride, int64_t heads, int D) {

@@ -44,6 +44,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "launch.cuh"
 
 namespace {
 
@@ -53,15 +54,11 @@ constexpr int kScoreThreads = 256;   // 8 warps x 8 pages per CTA
 constexpr int kPagesPerScoreCta = 64;
 constexpr int kKeysPerThread = 16;   // register-resident select: up to 4,096 past pages
 
-// Programmatic dependent launch (sm_90+): the query-mean kernel lets the
+// Programmatic dependent launch (launch.cuh): the query-mean kernel lets the
 // scores kernel launch once all of its CTAs have started; the scores kernel
 // does the work that does not read the query mean's output, then waits for
 // that grid to complete and its writes to be visible.  Without a dependent
 // launch the wait returns at once.
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Ticket of a CTA that has written its keys: one acquire-release atomic add
 // at GPU scope by one thread, between two CTA barriers.  The release covers
@@ -144,7 +141,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1) qmean_partial_kernel(
   constexpr int U = 16;               // rows in flight per thread
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
   const int Hkv = gridDim.y;
-  pdl_launch_dependents();
+  oomb::pdl_launch_dependents();
   // the next kernel on the stream counts finished CTAs from zero
   if (split == 0 && g == 0 && b == 0)
     for (int i = t; i < n_tickets; i += blockDim.x) tickets[i] = 0u;
@@ -596,8 +593,8 @@ __global__ void __launch_bounds__(kScoreThreads) qsum_reduce_kernel(
     const float* __restrict__ partial, int splits, float* __restrict__ qsum) {
   __shared__ float qs[2][D];
   const int g = blockIdx.x, b = blockIdx.y, Hkv = gridDim.x, t = threadIdx.x;
-  pdl_launch_dependents();
-  pdl_wait();
+  oomb::pdl_launch_dependents();
+  oomb::pdl_wait();
   reduce_partials<D, 32>(partial, splits, Hkv, b, g, qs);
   __syncthreads();
   if (t < D) qsum[(static_cast<size_t>(b) * Hkv + g) * D + t] = qs[0][t] + qs[1][t];
@@ -632,7 +629,7 @@ __global__ void __launch_bounds__(kScoreThreads, FUSED_SELECT ? 2 : 5) page_scor
   const int g = blockIdx.y, b = blockIdx.z, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int n_past = problem_npast(pb, b);
   const int n_ctas = max(1, (n_past + kPagesPerScoreCta - 1) / kPagesPerScoreCta);
-  if (!FUSED_SELECT) pdl_launch_dependents();
+  if (!FUSED_SELECT) oomb::pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) >= n_ctas) return;  // beyond this problem's pages
 
   // this warp's page summaries (EPL fp32 per lane and page).  One problem:
@@ -668,7 +665,7 @@ __global__ void __launch_bounds__(kScoreThreads, FUSED_SELECT ? 2 : 5) page_scor
   if (FUSED_SELECT) load_summaries();
 
   // the query-mean partials and the tickets it zeroed are read from here on
-  pdl_wait();
+  oomb::pdl_wait();
   // q_bar of (problem b, group g)
   if (FROM_QSUM) {
     if (t < D) qs[0][t] = __ldg(qsum + (static_cast<size_t>(b) * Hkv + g) * D + t);
@@ -750,7 +747,7 @@ __global__ void __launch_bounds__(kScoreThreads) topk_select_kernel(
   const unsigned long long* key_row = keys + row * key_stride(pb.max_past);
   const int max_sel = top_k + n_recent;
   int32_t* out_p = out_physical ? out_physical + row * max_sel : nullptr;
-  pdl_wait();  // the keys of the scores kernel
+  oomb::pdl_wait();  // the keys of the scores kernel
   if (n_past <= kScoreThreads * kKeysPerThread)
     select_pages_regs<kScoreThreads, kKeysPerThread>(key_row, page_table, n_past, top_k, n_recent,
                                                      num_pool_pages, out_logical + row * max_sel,
