@@ -22,6 +22,7 @@
 // in, and writes them as parts into its two slots of the workspace.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 
 #include "internal.h"
 #include "launch.cuh"
@@ -40,6 +41,8 @@ constexpr float kRescaleThreshold = 8.0f;
 
 constexpr int kOwnTile = 64;   // keys per tile of own_kernel
 constexpr int kPreTile = 128;  // keys, and rows, per tile of prefix_kernel
+constexpr int kPreSplit = 1, kPreOwn = 2;  // see pre_meta
+constexpr int kFewRows = 16;   // rows of a group that own_kernel takes in one pass over its keys
 
 struct DecodeParams {
   const __nv_bfloat16* q;
@@ -55,7 +58,7 @@ struct DecodeParams {
   int n_seqs, Hq, Hkv, G, P, max_pages, n_groups, max_prefix_pages, num_pages;
   int own_rows;   // query heads of a unit of own_kernel: 8 or 16
   int row_tiles;  // a sequence's units per KV head there
-  int pre_in_own; // the prefixes are units of own_kernel too
+  int own_group_rows; // groups of up to so many rows per KV head are units of own_kernel
   float scale_log2;
   // Workspace.  Part results are normalised O (fp32) and base-2 LSE.
   // own_meta [unit] {first CTA, CTAs}; slots [2 CTA + (0: begins before, 1: ends
@@ -66,8 +69,8 @@ struct DecodeParams {
   float* own_slot_lse;
   float* own_row_o;
   float* own_row_lse;
-  // of a prefix: [n_seqs Hq] {first CTA, 2 CTAs + whether the unit was split}; a slot
-  // per softmax lane; the second rows are lane 1's of a whole split unit
+  // of a prefix: [n_seqs Hq] {first CTA, 4 CTAs + kPreOwn of own_kernel's + kPreSplit of a
+  // split unit}; a slot per softmax lane; the second rows are lane 1's of a whole split unit
   int2* pre_meta;
   float* pre_slot_o;
   float* pre_slot_lse;
@@ -271,9 +274,9 @@ struct TileInfo {
 // of three (22.6 and 24.6 us); a separate warp for a unit's end costs the registers that
 // the third CTA needs.
 //
-// PRE: the prefixes' keys are units too, of up to kRows rows (sequence, query head)
-// of a group; items [0, n_groups) are groups, the others sequences.  A sequence is
-// the item of its own G rows.
+// PRE: the keys of prefixes with few rows are units too, of up to kRows rows (sequence,
+// query head) of a group; items [0, n_groups) are groups, the others sequences.  A sequence
+// is the item of its own G rows.
 constexpr int kOwnThreads = 160;
 template <bool PRE, int ROWS>
 struct OwnItem {
@@ -291,7 +294,7 @@ struct OwnItem {
       table = p.prefix_pages + static_cast<size_t>(i) * p.max_prefix_pages;
       rows = (hi - lo) * p.G;
       nt = tiles_of(len, kOwnTile);
-      row_tiles = (rows + ROWS - 1) / ROWS;
+      row_tiles = rows <= p.own_group_rows ? (rows + ROWS - 1) / ROWS : 0;
     } else {
       lo = PRE ? i - p.n_groups : i;
       len = checked_len(raw_len, p.max_pages, p.P, status);
@@ -454,7 +457,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
         const int over = it.nt - (n_mine - i);  // its tiles in later CTAs
         const int n = over <= 0 ? 1 : 1 + (over + per - 1) / per;
         if (PRE && item < p.n_groups) {
-          if (lane < rows) p.pre_meta[static_cast<size_t>(seq) * p.Hq + head] = make_int2(blockIdx.x, 2 * n);
+          if (lane < rows)
+            p.pre_meta[static_cast<size_t>(seq) * p.Hq + head] = make_int2(blockIdx.x, 4 * n + kPreOwn);
         } else if (lane == 0) {
           p.own_meta[(static_cast<size_t>(it.lo) * p.Hkv + g) * p.row_tiles + rt] =
               make_int2(blockIdx.x, n);
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
         }
         if (g == p.Hkv) {
           g = 0;
-          do {  // groups without keys or rows have no tiles
+          do {  // groups without keys or rows, and prefix_kernel's, have no tiles
             if (++item >= n_items) break;
             it.set(p, item, next_len, next_g0, next_g1, nullptr);
             first_id = 0;
@@ -782,8 +786,8 @@ struct PreWalk {
   __device__ __forceinline__ void load(const DecodeParams& p, uint32_t* status = nullptr) {
     gr = group_of(p, j, status);
     nt = tiles_of(gr.len, kPreTile);
-    row_tiles = static_cast<int>(
-        (static_cast<long long>(gr.hi - gr.lo) * p.G + kPreTile - 1) / kPreTile);
+    const int rows = (gr.hi - gr.lo) * p.G;
+    row_tiles = rows > p.own_group_rows ? (rows - 1) / kPreTile + 1 : 0;
   }
   __device__ __forceinline__ bool none() const { return nt == 0 || row_tiles == 0; }
   // steps and units of one KV head
@@ -1150,7 +1154,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       begins = w.step == 0;
       out_row = static_cast<size_t>(seq) * p.Hq + h;
       if (valid && begins && (ln == 0 || !w.split()))
-        p.pre_meta[out_row] = make_int2(blockIdx.x, 2 * w.parts(per) + w.split());
+        p.pre_meta[out_row] = make_int2(blockIdx.x, 4 * w.parts(per) + (w.split() ? kPreSplit : 0));
     };
     while (ok && w.next(p)) for (int i = 0; ok && i < w.here; ++i) {
       const bool split = w.split();
@@ -1409,7 +1413,8 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
     if (p.n_groups == 0 && own.y == 1) own.y = -1;
   }
   const bool work = active && own.y >= 0;
-  const int split = pre.y & 1, pre_ctas = pre.y >> 1;
+  const int split = pre.y & kPreSplit, pre_ctas = pre.y >> 2;
+  const bool pre_own = pre.y & kPreOwn;
   const int n = work ? own.y + (pre_ctas << split) : 0;
   const int own_row_in = h % p.G % p.own_rows;
   // where part k is: its row in the arrays of O and LSE
@@ -1426,18 +1431,18 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const Decod
       r.lse = (own.y == 1 ? p.own_row_lse : p.own_slot_lse) + at;
     } else {
       k -= own.y;
-      const int ln = split ? k & 1 : p.pre_in_own ? 0 : pre_row_in / kPreTile;
+      const int ln = split ? k & 1 : pre_own ? 0 : pre_row_in / kPreTile;
       const int c = k >> split;
       size_t slot = static_cast<size_t>(pre.x + c) * 2 + (c == 0);
-      if (!p.pre_in_own) slot = slot * 2 + ln;
+      if (!pre_own) slot = slot * 2 + ln;
       const size_t at = pre_ctas == 1   ? static_cast<size_t>(row)
-                        : p.pre_in_own ? slot * p.own_rows + pre_row_in % p.own_rows
+                        : pre_own ? slot * p.own_rows + pre_row_in % p.own_rows
                                        : slot * kPreTile + pre_row_in % kPreTile;
       r.o = (pre_ctas == 1  ? p.pre_row_o[split ? ln : 0]
-             : p.pre_in_own ? p.own_slot_o
+             : pre_own ? p.own_slot_o
                             : p.pre_slot_o) + at * D;
       r.lse = (pre_ctas == 1  ? p.pre_row_lse[split ? ln : 0]
-               : p.pre_in_own ? p.own_slot_lse
+               : pre_own ? p.own_slot_lse
                               : p.pre_slot_lse) + at;
     }
     return r;
@@ -1536,19 +1541,33 @@ bool good_shape(int32_t n_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t n_gr
          static_cast<int64_t>(n_seqs) * Hq <= INT32_MAX;
 }
 
-// Prefix groups of few rows (sequences x query heads per KV head, on average; rounded
-// down: a few sequences without a prefix do not count) are units of own_kernel:
-// prefix_kernel takes 128 rows' time for them, and is one more launch.  own_kernel reads
-// the keys again for every 16 rows, which long prefixes pay for.  Both ways, own_kernel
-// first, d = 128, 4 KV heads: 64 groups of 7 rows behind 500 tokens 27 and 39 us; 6 x 14
-// rows, 16000 tokens 54 and 60; 12 x 28 rows, 1200 tokens (12 tiles per SM) 25 and 29;
-// 12 x 28 rows, 4000 tokens (41 per SM) 54 and 51; 30 x 35 rows, 2000 tokens 92 and 57.
-bool prefixes_in_own(int n_seqs, int G, int Hkv, int n_groups, int64_t max_len, int sms) {
-  if (n_groups == 0) return false;
+// Groups of up to how many rows (sequences x query heads per KV head) are units of
+// own_kernel: none (0), those of one pass over their keys (kFewRows), all (INT_MAX).  The
+// kernels look at each group's own size; the host, which does not know the sizes, decides
+// whether prefix_kernel is launched at all, from the rows of a group on average and the
+// length that prefix_pages has room for.  prefix_kernel takes 128 rows' time for a few, and
+// is one more launch; own_kernel reads the keys again for every 16 rows.
+// Both ways for equal groups, own_kernel first, d = 128, 4 KV heads: 64 groups of 7 rows
+// behind 500 tokens 27 and 39 us; 6 x 14 rows, 16000 tokens 54 and 60; 12 x 28 rows, 1200
+// tokens (12 tiles per SM) 25 and 29; 12 x 28 rows, 4000 tokens (41 per SM) 54 and 51; 30 x
+// 35 rows, 2000 tokens 92 and 57.  At 17 to 32 rows the bound on the tiles also bounds what one
+// group with all of them would take (48 sequences of 7 rows in one of 12 groups, 1200 tokens,
+// 26 and 24).
+// Few rows on average: if one group had all of them, its passes would take own_kernel, and
+// both kernels with each group where it belongs: 210 rows, 500 tokens (3 tiles per SM) 18
+// and 20 us; 210 rows, 1000 tokens (6) 28 and 22; 420 rows, 1000 tokens (12) 55 and 28; 1400
+// rows, 32773 tokens 1374 and 124.  With both, equal small groups pay 2-3 us for the launch
+// (100 of 7 rows, 8000 tokens 406 and 409; 16 of 14 rows, 1000 tokens, 14 per SM, 18 and 20).
+// Many rows on average because most sequences have no prefix: prefix_kernel, 6-8 us
+// more (4 groups of 7 rows behind 2000 tokens, 96 sequences without 20 and 26; 64 behind 500,
+// 336 without 47 and 54).
+int prefix_rows_in_own(int n_seqs, int G, int Hkv, int n_groups, int64_t max_len, int sms) {
+  if (n_groups == 0) return 0;
   const int64_t rows = static_cast<int64_t>(n_seqs / n_groups) * G;
-  if (rows <= 16) return true;
-  const int64_t tiles = 2ll * n_groups * Hkv * ((max_len + kOwnTile - 1) / kOwnTile);
-  return rows <= 32 && tiles <= 16ll * sms;
+  const int64_t tiles = Hkv * ((max_len + kOwnTile - 1) / kOwnTile);  // of one pass, one group
+  if (rows > kFewRows) return rows <= 32 && 2 * n_groups * tiles <= 16ll * sms ? INT_MAX : 0;
+  const int64_t passes = (static_cast<int64_t>(n_seqs) * G + kFewRows - 1) / kFewRows;
+  return passes <= 1 || passes * tiles <= 8ll * sms ? INT_MAX : kFewRows;
 }
 // Rows of a unit of own_kernel: one column of 8, or two.
 int own_unit_rows(int G, bool pre) { return G <= 8 && !pre ? 8 : 16; }
@@ -1558,8 +1577,8 @@ int own_ctas(int sms, int D, int rows) {
 }
 
 // Lays the workspace out from `base` (null: only counts) and returns its bytes.
-size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, bool pre_in_own,
-               int sms, DecodeParams* p) {
+size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups,
+               int own_group_rows, int sms, DecodeParams* p) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* r = base ? base + at : nullptr;
@@ -1568,8 +1587,8 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   };
   const size_t rows = static_cast<size_t>(n_seqs) * Hq;
   const int G = Hq / Hkv;
-  p->pre_in_own = pre_in_own;
-  p->own_rows = own_unit_rows(G, p->pre_in_own);
+  p->own_group_rows = own_group_rows;
+  p->own_rows = own_unit_rows(G, own_group_rows > 0);
   p->row_tiles = (G + p->own_rows - 1) / p->own_rows;
   const size_t own_rows = 2 * static_cast<size_t>(own_ctas(sms, D, p->own_rows)) * p->own_rows;
   const size_t pre_rows = 4 * static_cast<size_t>(sms) * kPreTile;
@@ -1583,11 +1602,12 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
     p->own_row_o = reinterpret_cast<float*>(take(rows * D * 4));
     p->own_row_lse = reinterpret_cast<float*>(take(rows * 4));
     p->pre_meta = reinterpret_cast<int2*>(take(rows * 8));
-    if (!p->pre_in_own) {
+    const bool prefix = own_group_rows < INT_MAX;
+    if (prefix) {
       p->pre_slot_o = reinterpret_cast<float*>(take(pre_rows * D * 4));
       p->pre_slot_lse = reinterpret_cast<float*>(take(pre_rows * 4));
     }
-    for (int ln = 0; ln < (p->pre_in_own ? 1 : 2); ++ln) {
+    for (int ln = 0; ln < (prefix ? 2 : 1); ++ln) {
       p->pre_row_o[ln] = reinterpret_cast<float*>(take(rows * D * 4));
       p->pre_row_lse[ln] = reinterpret_cast<float*>(take(rows * 4));
     }
@@ -1595,13 +1615,14 @@ size_t lay_out(uint8_t* base, int n_seqs, int Hq, int Hkv, int D, int n_groups, 
   return at;
 }
 
-// Bytes of the workspace: enough for either way with the prefixes, which also goes by
+// Bytes of the workspace: enough for every way with the prefixes, which also goes by
 // lengths that are not known here.
 size_t workspace_bytes(int n_seqs, int Hq, int Hkv, int D, int n_groups, int sms) {
   DecodeParams p;
   size_t bytes = 0;
-  for (int own = 0; own < (n_groups > 0 ? 2 : 1); ++own)
-    bytes = std::max(bytes, lay_out(nullptr, n_seqs, Hq, Hkv, D, n_groups, own, sms, &p));
+  for (int own_group_rows : {0, kFewRows, INT_MAX})
+    if (own_group_rows == 0 || n_groups > 0)
+      bytes = std::max(bytes, lay_out(nullptr, n_seqs, Hq, Hkv, D, n_groups, own_group_rows, sms, &p));
   return bytes;
 }
 
@@ -1639,7 +1660,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
   cfg.attrs = attr;
   cudaError_t e = cudaSuccess;
   CUtensorMap map;
-  const bool prefix = p.n_groups > 0 && !p.pre_in_own;
+  const bool prefix = p.n_groups > 0 && p.own_group_rows < INT_MAX;
   if (prefix) {
     if (!kv_map(&map, pool, p.P, 1)) return OOMB_ERR_CUDA;
     cfg.gridDim = dim3(sms);
@@ -1654,7 +1675,7 @@ oomb_status launch(const oomb_pool* pool, const DecodeParams& p, int sms, cudaSt
     cfg.blockDim = dim3(kOwnThreads);
     cfg.numAttrs = prefix ? 1 : 0;
     cfg.dynamicSmemBytes = p.own_rows == 8 ? OwnCfg<D, 1>::kSmem : OwnCfg<D, 2>::kSmem;
-    e = p.pre_in_own      ? cudaLaunchKernelEx(&cfg, own_kernel<D, 2, true>, p, map)
+    e = p.own_group_rows  ? cudaLaunchKernelEx(&cfg, own_kernel<D, 2, true>, p, map)
         : p.own_rows == 8 ? cudaLaunchKernelEx(&cfg, own_kernel<D, 1, false>, p, map)
                           : cudaLaunchKernelEx(&cfg, own_kernel<D, 2, false>, p, map);
   }
@@ -1712,14 +1733,14 @@ extern "C" oomb_status oomb_decode_attn(oomb_pool* pool, const oomb_decode_args*
     return OOMB_ERR_INVALID_ARG;
   DecodeParams p;
   const int sms = sm_count(d.device);
-  const bool pre_in_own =
-      prefixes_in_own(a->n_seqs, Hq / d.num_kv_heads, d.num_kv_heads, a->n_groups,
-                      static_cast<int64_t>(a->max_prefix_pages) * d.page_size, sms);
+  const int own_group_rows =
+      prefix_rows_in_own(a->n_seqs, Hq / d.num_kv_heads, d.num_kv_heads, a->n_groups,
+                         static_cast<int64_t>(a->max_prefix_pages) * d.page_size, sms);
   if (!a->workspace || !aligned16(a->workspace) ||
       a->workspace_bytes < workspace_bytes(a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups, sms))
     return OOMB_ERR_INVALID_ARG;
   lay_out(static_cast<uint8_t*>(a->workspace), a->n_seqs, Hq, d.num_kv_heads, D, a->n_groups,
-          pre_in_own, sms, &p);
+          own_group_rows, sms, &p);
   p.q = static_cast<const __nv_bfloat16*>(a->q);
   p.o = static_cast<__nv_bfloat16*>(a->o);
   p.lse = a->lse;
