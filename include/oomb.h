@@ -294,7 +294,7 @@ oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args,
  * their own) in the pages prefix_pages[j]; sequences before group_start[0] and
  * from group_start[n_groups] on have no prefix.  The prefix and a sequence's
  * own pages may share pages.  A sequence without any token gets O = 0 and
- * LSE = -inf.
+ * LSE = -inf, and so does a head whose every score is -infinity.
  * P is rounded to bf16 for the product with V; S, the running maximum and sum,
  * O and the merge of the parts are fp32.  Results do not depend on what else
  * runs and are the same bits in every call on the same inputs.
