@@ -239,7 +239,10 @@ oomb_status oomb_chunk_attn_bwd_step(oomb_pool* pool, const oomb_attn_args* args
  *   stay as they were.  A token whose page id is outside the pool sets bit 0 of
  *   the device status word; one whose page index is outside [0, max_pages), a
  *   negative cached_lens and a seq_start that decreases or leaves [0, n_tokens]
- *   set bit 2.  Such tokens' keys and values are skipped.
+ *   set bit 2.  Such tokens' keys and values are skipped; their queries are rotated all
+ *   the same, but for a bad seq_start, whose tokens are skipped like those outside every
+ *   sequence.  A sequence with skipped tokens may miss the representative of the page in
+ *   which the others end.
  * Two tokens of one call must not share a cache position, and pages that one
  * call writes must belong to one sequence each.  One or two launches.
  *

@@ -335,3 +335,46 @@ def test_refusals_leave_everything_untouched():
         with pytest.raises(TypeError):
             pk.kv_append_rope(pg.pool, k, v, starts.long(), *args[1:])
         assert (pg.kv == 1.0).all()
+
+
+@pytest.mark.parametrize("n", [8, 900])  # one launch, and two
+def test_tokens_of_bad_starts_leave_queries_and_gradients_as_they_were(n):
+    """Tokens of a sequence whose start decreases or ends behind the batch are skipped with
+    their queries; those of bad pages, lengths and tables only with keys and values."""
+    rng = np.random.default_rng(14)
+    f = torch.from_numpy(_freq(64)).to(DEV)
+    k, v, q = (bf16(rng, n, 1, 64).to(DEV) for _ in range(3))
+    pos, P, h, t = i32(list(range(n))), 16, n // 2, 3 * n // 4
+    width = -(-n // P) + 1
+    with Pages(2 * width, P, 1, 64, True) as pg:
+        pages = [list(range(width)), list(range(width, 2 * width))]
+        want = torch.empty_like(q)
+        pk.kv_append_rope(pg.pool, k, v, i32([0, n]), i32([0]), i32(pages[:1]), pos, f, q=q, q_out=want)
+        torch.cuda.synchronize()
+        assert pg.status() == 0
+        none, out = list(pages), [[-1] * width, pages[1]]
+        for starts, cached, table, status, queries, tokens in (
+                ([0, h, n + 1], [0, 0], none, 4, h, h),         # ends behind the batch
+                ([0, t, h], [0, 0], none, 4, h, h),             # decreases: [h, t) are nobody's
+                ([-1, h, n], [0, 0], none, 4, (h, n), (h, n)),  # begins before it
+                ([0, h, n], [0, 0], out, 1, n, (h, n)),
+                ([0, h, n], [-1, 0], none, 4, n, (h, n)),
+                ([0, h, n], [2**31 - 1, 0], none, 4, n, (h, n))):
+            bounds = [x if isinstance(x, tuple) else (0, x) for x in (queries, tokens)]
+            (qa, qb), (ka, kb) = bounds
+            args = (i32(starts), i32(cached), i32(table), pos, f)
+            got = torch.full_like(q, 3.0)
+            pk.kv_append_rope(pg.pool, k, v, *args, q=q, q_out=got)
+            torch.cuda.synchronize()
+            assert pg.status() == status
+            assert torch.equal(got[qa:qb], want[qa:qb])
+            assert (got[:qa] == 3.0).all() and (got[qb:] == 3.0).all()
+            pg.grad.fill_(1.0)
+            dk, dv, dq = (torch.full_like(k, 3.0) for _ in range(3))
+            pk.kv_append_rope_bwd(pg.pool, dk, dv, *args, dq=q, dq_out=dq)
+            torch.cuda.synchronize()
+            assert pg.status() == status
+            assert (dv[ka:kb] == 1.0).all() and (dk[ka:kb] != 3.0).any(dim=-1).all()
+            assert (dq[qa:qb] != 3.0).any(dim=-1).all()
+            for x, (a, b) in ((dk, (ka, kb)), (dv, (ka, kb)), (dq, (qa, qb))):
+                assert (x[:a] == 3.0).all() and (x[b:] == 3.0).all()
