@@ -286,7 +286,8 @@ oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args,
 /* ---------------------------------------------------------------- single-token attention
  * oomb_decode_attn: one query token per sequence attends to the tokens of the
  * sequence's own pages and, if it is in a prefix group, to the group's prefix,
- * whose pages are stored once and read once for all sequences of the group:
+ * whose pages are stored once for all sequences of the group and read once for every
+ * 256 rows (sequence, query head of a KV head) of it, or every 16 where groups are small:
  *   S_j = scale q.k_j over both,  LSE = ln sum_j exp(S_j),  O = sum_j exp(S_j - LSE) v_j.
  * Sequence b has seq_lens[b] own tokens (0 allowed) in the pages page_tables[b]
  * in order; the last page may be partly filled, what its other rows hold
@@ -300,7 +301,10 @@ oomb_status oomb_kv_append_rope_bwd(oomb_pool* pool, const oomb_rope_args* args,
  * LSE = -inf, and so does a head whose every score is -infinity.
  * P is rounded to bf16 for the product with V; S, the running maximum and sum,
  * O and the merge of the parts are fp32.  Results do not depend on what else
- * runs and are the same bits in every call on the same inputs.
+ * runs and are the same bits in every call on the same inputs.  In another batch,
+ * or with another max_prefix_pages (the longest prefix that the call reckons with
+ * when it chooses its kernels), a sequence's sums may be rounded in another order.
+ * Own keys are read once for every 16 query heads of a KV head.
  * Lengths and group starts are read on the device, so a captured graph replays
  * with new ones.  A length outside [0, max_pages * page_size] is clamped and
  * sets bit 2 of the device status word, as does a group_start that decreases or

@@ -434,8 +434,8 @@ def decode_attn(pool, q, o, page_tables, seq_lens, softmax_scale, workspace, lse
     """oomb_decode_attn: one query token per sequence (q, o [n_seqs][Hq][d] bf16, rows
     may stand apart) over the first seq_lens[b] tokens of the pages page_tables[b]
     and, with prefix_pages [n_groups][max_prefix_pages], prefix_lens [n_groups] and
-    group_start [n_groups + 1], over the prefix of the sequence's group, computed
-    once for the group.  lse: optional fp32 [n_seqs][Hq] output."""
+    group_start [n_groups + 1], over the prefix of the sequence's group, whose keys are
+    read for many of the group's rows at once.  lse: optional fp32 [n_seqs][Hq] output."""
     dev, shape = _heads_of(q, "q")
     (n, hq, D), i32 = shape, torch.int32
     qp, qs = _rows(q, shape, dev, "q")

@@ -135,3 +135,20 @@ def test_starts_that_decrease_or_overlap_stay_within_the_call():
             else:  # sequences behind every group have their own keys alone
                 b.starts = [0] * (groups + 1)
                 b.check(o, lse, only=range(max(starts), n))
+
+
+def test_a_wider_prefix_table_changes_the_rounding_at_most():
+    """The longest prefix that the table has room for picks the kernel: both are right."""
+    with Batch(14, 2, 128, 64, [33] * 60, [*((i, 100) for i in range(60)), (60, None)],
+               seed=45) as b:
+        pages, lens, kw = b.args()
+        narrow = kw["prefix_pages"]
+        for width in (narrow.shape[1], 64):
+            wide = torch.full((60, width), -1, dtype=torch.int32, device=DEV)
+            wide[:, :narrow.shape[1]] = narrow
+            o, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=DEV)
+            pk.decode_attn(b.pg.pool, b.q, o, pages, lens, b.scale, b.workspace(), lse=lse,
+                           **{**kw, "prefix_pages": wide})
+            torch.cuda.synchronize()
+            assert b.pg.status() == 0
+            b.check(o, lse, only=range(0, 60, 3))
