@@ -21,6 +21,12 @@
 // CTA, whatever the lengths are.  A unit that lies inside one range is whole;
 // of the others a CTA has at most two, the one it begins in and the one it ends
 // in, and writes them as parts into its two slots of the workspace.
+//
+// Rounding.  P goes to the product with V in bf16, V's type, as in the chunk attention: the
+// tensor cores take both operands of one type, and P as two bf16 terms would double the
+// products.  It costs the result 0.0017-0.0023 (relative L2 against 64 bits) where P in 32
+// bits has 0.0016-0.0017, nearly all of it the rounding of the bf16 output.  Sums take the
+// unrounded p; scores, maxima, sums, O and the merge are fp32.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -269,8 +275,8 @@ struct TileInfo {
 // both per 64 columns).  The number of barriers does not depend on what is found, so
 // a wait that gives up leaves nobody behind.
 // Bound by memory where sequences are long: 3 x 100-131 thousand keys (745 MB) take
-// 113-116 us, 6.4-6.6 TB/s.  A ragged batch (48 sequences, 103 MB) takes 22.3-23.0 us
-// alone, 4.5 TB/s: CTAs have 7 tiles each, and their start, the look at lengths and pages,
+// 113-116 us, 6.4-6.6 TB/s.  A ragged batch (48 sequences, 103 MB) takes 22.0-22.8 us
+// alone, 4.6 TB/s: CTAs have 7 tiles each, and their start, the look at lengths and pages,
 // takes as long as three.  Three CTAs of two tiles each keep more loads under way than two
 // of three (22.6 and 24.6 us); a separate warp for a unit's end costs the registers that
 // the third CTA needs.
@@ -692,7 +698,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<D, NT>::kCtasPerSm)
           const float2 x = *reinterpret_cast<const float2*>(&sl[n_units & 1][w][n * 8 + hd]);
           total = make_float2(total.x + x.x, total.y + x.y);
         }
-        // a sum is 0 without keys, and NaN (which stays) with a score of NaN or +inf
+        // a sum is 0 without keys, and NaN (which stays) with a score of NaN or +inf; others are
+        // between 1 (the key of the maximum) and 2^8 times the number of keys, where the quick quotient is good to
+        // 2 ulp and the quick logarithm to 2^-21, far below the output's step
         const float i0 = total.x != 0.f ? __fdividef(1.f, total.x) : 0.f;
         const float i1 = total.y != 0.f ? __fdividef(1.f, total.y) : 0.f;
         if (warp == 0 && lane < 4) {
@@ -918,8 +926,8 @@ __device__ __forceinline__ void reg_dec() {
 // their first half), O [256,384) [384,512).  Q is in shared memory, written by its
 // lane's threads.
 // Bound by the tensor cores' clock and the chain of a step for many rows: 256 sequences
-// behind 32773 tokens (1792 rows per KV head, 120 GFLOP) take about 125 us at 1.6 GHz
-// (1.9 without this load), 960 TFLOP/s.  No one part holds it up: without the exponentials
+// behind 32773 tokens (1792 rows per KV head, 120 GFLOP) take about 129 us at 1.64 GHz
+// (1.9 without this load), 930 TFLOP/s.  No one part holds it up: without the exponentials
 // the call takes 127 instead of 135 us, without the loads 129, with an eighth of the PV
 // products 131.  Two threads per row (139), exponentials by a polynomial for a part of the
 // row (137-164), asking for barriers ahead of time (168) and a product warp per lane (174)
@@ -978,7 +986,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (warp >= 8) {
     // 208 and 88 registers: with 224 and 56 (216 and 72) these warps spill, to L2, as shared
     // memory leaves no L1: 256 sequences behind 32773 tokens 145 (145) us, now 135; with 200
-    // and 104 the softmax does, 138 us
+    // and 104 the softmax does, 138 us.  For d = 64, which has not been measured apart, the
+    // kernel spills 164 bytes with this split
     reg_dec<88>();
     if (warp == 8) {
       // ---------------------------------------------------------- loads
@@ -1382,8 +1391,8 @@ __device__ __forceinline__ int find_group(const DecodeParams& p, int b) {
 
 // W warps per row (sequence, head); a lane takes 4 values of a part, a warp
 // 128 / D parts at once.  Bound by latency: its launch (a dependent one), the look for a
-// row's parts, then the parts, four at a time.  Alone 6.3-6.9 us with 84 rows of up to 150
-// parts (W 16) or 1344 rows (W 4), 15 us with 7168 rows of about 10 parts from DRAM
+// row's parts, then the parts, four at a time.  Alone 5.5-6.9 us with 84 rows of up to 150
+// parts (W 16) or 1344 rows (W 4), 14 us with 7168 rows of about 10 parts from DRAM
 // (W 1, 27 MB); in a call the parts come from L2.
 template <int D, int W>
 __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) merge_kernel(const DecodeParams p) {

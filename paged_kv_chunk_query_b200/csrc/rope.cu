@@ -288,8 +288,8 @@ __device__ __forceinline__ void mean_of_page(const RopeParams& p, int tok, int p
 // of each head, values [ea, ea + 8) and [eb, eb + 8), chosen so that eight pairs lie in
 // them.  The loads of a warp's first piece are issued before the angles and places are
 // known.
-// A chunk of 4096 tokens (28 query, 4 KV heads of 128) moves 92 MB in 17.8-18.5 us alone
-// and cold (5.0 TB/s), its backward 84 MB in 17.2-17.5 (4.8 TB/s).  Between the floor and
+// A chunk of 4096 tokens (28 query, 4 KV heads of 128) moves 92 MB in 16.6-17.4 us alone
+// and cold (5.3-5.5 TB/s), its backward 84 MB in 16.4-16.5 (5.1 TB/s).  Between the floor and
 // this stand the start (places and angles, about 3 us before the first store) and the
 // issue slots (57% used).  One wave of CTAs, four per SM: three, or seven warps each so
 // that the mean kernel fits beside, were slower (24.6 us with the means, now 20.5).
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, MEAN ? kMeanCtas : 4) rope_kernel(co
 // token in its tile takes it.  Keys are summed anew rather than added to the old mean:
 // a sequence that was cut back to fewer tokens and went on gets the right mean, and
 // the call can be repeated.  One warp per (page, head), or up to 16 where a CTA has
-// few of them: the load latency of 64 rows is then paid once.  Bound by latency: 8.4-9.0 us
+// few of them: the load latency of 64 rows is then paid once.  Bound by latency: 7.3-7.8 us
 // alone for a chunk of 4096 tokens, about 5 behind rope_kernel.  A single launch in which a
 // CTA owns a page's keys and values needs none of this, but is uneven: the chunk took
 // 28-30 us.  A ticket per page, by which the last of its CTAs takes the mean, is no faster
