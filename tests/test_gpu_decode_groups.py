@@ -152,3 +152,40 @@ def test_a_wider_prefix_table_changes_the_rounding_at_most():
             torch.cuda.synchronize()
             assert b.pg.status() == 0
             b.check(o, lse, only=range(0, 60, 3))
+
+
+@pytest.mark.parametrize("groups", [0, 1, 65535])
+def test_the_largest_batch(groups):
+    """65535 sequences of 0 to 3 own tokens, all in a few pages, behind no prefix, one for
+    all, or a group each."""
+    n, P, d = 65535, 16, 64
+    rng = np.random.default_rng(46)
+    with Batch(2, 1, d, P, [3] * 7, [(0, 40), (3, 16), (7, None)], seed=46) as b:
+        lens = rng.integers(0, 4, n)
+        which = rng.integers(0, 7, n)
+        own = torch.tensor([x[0][0] for x in b.own], dtype=torch.int32)
+        q = torch.randn(n, 2, d, device=DEV).bfloat16()
+        kw, pre = {}, np.zeros(n, np.int64)
+        if groups:
+            behind = rng.integers(0, 2, groups)
+            size = np.array([40, 16])[behind]
+            pages = torch.tensor([(list(x[0]) + [-1] * 3)[:3] for x in b.shared], dtype=torch.int32)
+            starts = [0, n] if groups == 1 else list(range(n + 1))
+            kw = dict(prefix_pages=pages[torch.from_numpy(behind)].to(DEV),
+                      prefix_lens=i32(size.tolist()), group_start=i32(starts))
+            pre = np.repeat(behind, n) if groups == 1 else behind
+        o, lse = torch.empty_like(q), torch.empty(n, 2, device=DEV)
+        ws = torch.empty(pk.decode_attn_workspace_size(n, 2, 1, d, groups), dtype=torch.uint8,
+                         device=DEV)
+        pk.decode_attn(b.pg.pool, q, o, own[torch.from_numpy(which)].reshape(n, 1).to(DEV),
+                       i32(lens.tolist()), b.scale, ws, lse=lse, **kw)
+        torch.cuda.synchronize()
+        assert b.pg.status() == 0
+        # a sample of them as a batch of their own, for the oracle
+        some = [0, 1, *rng.integers(2, n - 1, 60).tolist(), n - 1]
+        b.own = [(b.own[w][0], b.own[w][1][:m], b.own[w][2][:m])
+                 for w, m in zip(which[some], lens[some])]
+        b.shared = [b.shared[pre[i]] for i in some] if groups else []
+        b.starts = list(range(len(some) + 1)) if groups else []
+        b.lens = lens[some].tolist()
+        b.check(o[some], lse[some], q=q[some])
